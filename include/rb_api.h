@@ -71,7 +71,9 @@ typedef enum {
     RB_ERR_DEVICE = 6         /* a kernel reported a failure through its flag */
 } rb_status;
 
-typedef enum { RB_F32 = 0, RB_F16 = 1 } rb_dtype;
+/* RB_BF16 is taken by the 8-bit block and gradient calls at the end of this
+ * header only; the others refuse it with RB_ERR_INVALID_ARG. */
+typedef enum { RB_F32 = 0, RB_F16 = 1, RB_BF16 = 2 } rb_dtype;
 
 typedef enum { RB_ROWS = 0, RB_SLICED = 1 } rb_order;
 
@@ -392,6 +394,106 @@ RB_API rb_status rb_gemv_noalloc(const uint32_t* planes, const void* alpha, rb_d
  * scratch on the current device (the last noalloc call there).
  */
 RB_API rb_status rb_gemv_check(const void* workspace, void* stream);
+
+/*
+ * 8-bit blocks and the backward pass
+ * ----------------------------------
+ * One storage format serves the layers that a residual-binary model keeps at
+ * 8 bits and the activations that a training step keeps for its backward
+ * pass: e4m3 codes (one byte: sign, 4 exponent bits, 3 mantissa bits, largest
+ * value 448, 0x7f and 0xff NaN; row-major [rows][K], dense) and one fp32 scale
+ * for each block of block_rows x 128 of them, [ceil(rows / block_rows)][K / 128];
+ * a value is code * scale. block_rows is 1 (activations) or 128 (weights; the
+ * last block may have fewer rows). K is a positive multiple of 128, and
+ * rows * (K / 128) < 2^31.
+ */
+
+/*
+ * rb_pack8 -- codes and scales of X. Per block, with A the largest finite
+ * magnitude in it:
+ *     n = the smallest integer >= -126 with A <= 448 * 2^n (0 if A = 0),
+ *     scale = 2^n,   code = the e4m3 value nearest to x / scale (ties to even).
+ * Where n is the largest that X's type can need (8 for fp16, 120 for bf16 and
+ * fp32), codes stop at +-240, so that code * scale stays finite in that type.
+ * A value that is not finite becomes a NaN code and does not count for A.
+ * (A power of two makes code * scale exact, in a 16-bit type as well.)
+ *
+ * X       device, rows x K values of x_dtype (RB_F32, RB_F16 or RB_BF16), row
+ *         pitch ldx elements (>= K); base and row pitch 16-byte aligned.
+ * codes   device, out, rows * K bytes, 16-byte aligned.
+ * scales  device, out, ceil(rows / block_rows) * (K / 128) fp32 values.
+ */
+RB_API rb_status rb_pack8(const void* X, rb_dtype x_dtype, int64_t ldx, int64_t rows, int64_t K, int32_t block_rows,
+                          uint8_t* codes, float* scales, void* stream);
+
+/*
+ * rb_unpack8 -- X = code * scale in fp32, rounded to x_dtype (exact for what
+ * rb_pack8 wrote from a tensor of that type). Arguments as rb_pack8; X is
+ * written, the columns between K and ldx are not.
+ */
+RB_API rb_status rb_unpack8(const uint8_t* codes, const float* scales, int64_t rows, int64_t K, int32_t block_rows,
+                            void* X, rb_dtype x_dtype, int64_t ldx, void* stream);
+
+/*
+ * rb_gemm8 -- Y_t = W X_t for a layer kept at 8 bits, on the tcgen05 tensor
+ * cores, any number of tokens:
+ *     y[t][m] = sum_g xs[t][g] ws[m / 128][g] sum_{j in block g} x[t][j] w[m][j]
+ * (g = 0 .. K / 128 - 1), every sum in fp32. Scales may be any fp32 values.
+ *
+ * w, w_scales  device, [M][K] codes and [ceil(M / 128)][K / 128] scales
+ *              (rb_pack8 with block_rows = 128); codes 16-byte aligned.
+ * x, x_scales  device, [T][K] codes and [T][K / 128] scales (block_rows = 1).
+ * Y            device, out, [T][ldy] of y_dtype, ldy >= M.
+ * T            1..2^22.
+ * workspace    at least 256 bytes, 16-byte aligned: the header with the error
+ *              word that rb_gemm_check reads. Nothing needs to be zero.
+ * Errors: as rb_gemm.
+ */
+RB_API rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t* x, const float* x_scales, int64_t M,
+                          int64_t K, int32_t T, void* Y, rb_dtype y_dtype, int64_t ldy, void* workspace, size_t ws_bytes,
+                          void* stream);
+
+/*
+ * rb_gemm_wgrad -- the weight gradient of a linear layer whose input was kept
+ * in 8 bits:  dW = add + dY^T X,  X[t][j] = codes[t][j] scales[t][j / 128].
+ * It is the full gradient to the shared weight W (RaBiT section 4.2: every
+ * path is derived from one weight, which receives the gradient of the
+ * reconstructed one).
+ *
+ * dY      device, [T][ldd] of dy_dtype (RB_F16 or RB_BF16), M columns; base and
+ *         row pitch 16-byte aligned.
+ * codes, scales  device, [T][K] and [T][K / 128] (rb_pack8, block_rows = 1).
+ *         X enters the product in dY's type: code * scale rounded to it, which
+ *         is exact for what rb_pack8 wrote from a tensor of that type.
+ * add     device, nullable, M x K values of dw_dtype with pitch ldw, added
+ *         before the one rounding to dw_dtype; may be dW itself (gradients
+ *         summed over micro-batches).
+ * dW      device, out, [M][ldw] of dw_dtype (any rb_dtype), ldw >= K.
+ * T       1..2^22. workspace, errors: as rb_gemm8.
+ */
+RB_API rb_status rb_gemm_wgrad(const void* dY, rb_dtype dy_dtype, int64_t ldd, int64_t M, const uint8_t* codes,
+                               const float* scales, int64_t K, int32_t T, const void* add, void* dW, rb_dtype dw_dtype,
+                               int64_t ldw, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * rb_gemm_dgrad -- the gradient of rb_gemm with respect to its input:
+ *     dX[t][j] = sum_i dY[t][i] W^[i][j],   W^ = sum_k alpha_k (.) B_k
+ * straight from the sign planes: neither W^ nor its transpose is stored.
+ * W^[i][j] (the sum of the fp32 values of its scales) is rounded once to dY's
+ * type, so a result is within eps / 2 * sum_i |dY[t][i] W^[i][j]| (eps / 2 =
+ * 2^-11 for fp16, 2^-8 for bf16) of the unrounded product, plus fp32 sums and
+ * the rounding to dx_dtype.
+ *
+ * planes, alpha, alpha_dtype, L  as rb_gemm; 1..4 paths; scales RB_F32 or
+ *         RB_F16 in either grouping.
+ * dY      device, [T][ldd] of dy_dtype (RB_F16 or RB_BF16), L.M columns; base
+ *         and row pitch 16-byte aligned.
+ * dX      device, out, [T][ldx] of dx_dtype (any rb_dtype), ldx >= L.K.
+ * T       1..2^22. workspace, errors: as rb_gemm8.
+ */
+RB_API rb_status rb_gemm_dgrad(const uint32_t* planes, const void* alpha, rb_dtype alpha_dtype, rb_layout L,
+                               const void* dY, rb_dtype dy_dtype, int64_t ldd, int32_t T, void* dX, rb_dtype dx_dtype,
+                               int64_t ldx, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "librb.so")
 RB_OK = 0
 STATUS_NAMES = {0: "RB_OK", 1: "RB_ERR_INVALID_ARG", 2: "RB_ERR_UNSUPPORTED", 3: "RB_ERR_ALIGNMENT",
                 4: "RB_ERR_WORKSPACE", 5: "RB_ERR_CUDA", 6: "RB_ERR_DEVICE"}
-RB_F32, RB_F16 = 0, 1
+RB_F32, RB_F16, RB_BF16 = 0, 1, 2
 RB_ROWS, RB_SLICED = 0, 1
 
 # every symbol include/rb_api.h declares
@@ -26,7 +26,8 @@ EXPORTED = ("rb_planes_words", "rb_scales_count", "rb_status_string", "rb_last_e
             "rb_gemm", "rb_gemm_workspace_bytes", "rb_gemm_check",
             "rb_pack_fixed", "rb_dual_gemv", "rb_dual_gemv_workspace_bytes", "rb_gemm_reconstruct",
             "rb_gemv_swiglu", "rb_gemv_swiglu_workspace_bytes", "rb_gemm_from_weight",
-            "rb_gemm_from_weight_workspace_bytes")
+            "rb_gemm_from_weight_workspace_bytes",
+            "rb_pack8", "rb_unpack8", "rb_gemm8", "rb_gemm_wgrad", "rb_gemm_dgrad")
 
 
 class RbError(RuntimeError):
@@ -106,6 +107,16 @@ def load() -> ctypes.CDLL:
         lib.rb_dual_gemv.restype = st
         lib.rb_dual_gemv_workspace_bytes.argtypes = [Layout, i32]
         lib.rb_dual_gemv_workspace_bytes.restype = sz
+        lib.rb_pack8.argtypes = [vp, st, i64, i64, i64, i32, vp, vp, vp]
+        lib.rb_pack8.restype = st
+        lib.rb_unpack8.argtypes = [vp, vp, i64, i64, i32, vp, st, i64, vp]
+        lib.rb_unpack8.restype = st
+        lib.rb_gemm8.argtypes = [vp, vp, vp, vp, i64, i64, i32, vp, st, i64, vp, sz, vp]
+        lib.rb_gemm8.restype = st
+        lib.rb_gemm_wgrad.argtypes = [vp, st, i64, i64, vp, vp, i64, i32, vp, vp, st, i64, vp, sz, vp]
+        lib.rb_gemm_wgrad.restype = st
+        lib.rb_gemm_dgrad.argtypes = [vp, vp, st, Layout, vp, st, i64, i32, vp, st, i64, vp, sz, vp]
+        lib.rb_gemm_dgrad.restype = st
         _lib = lib
         return lib
 

@@ -402,3 +402,195 @@ def dual_gemv(planes: torch.Tensor, h: torch.Tensor, g: Optional[torch.Tensor], 
         if check_device:
             check(lib.rb_gemv_check(_p(workspace), _stream(dev)))
     return y
+
+
+_DT8 = {torch.float32: _lib.RB_F32, torch.float16: _lib.RB_F16, torch.bfloat16: _lib.RB_BF16}
+_HEADER_BYTES = 256     # workspace of the calls below: the header with the error word
+
+
+def _call(dev: torch.device, fn, *args) -> None:
+    """fn(*args, stream) on the current stream of `dev`, whichever device is current."""
+    if torch.cuda.current_device() == dev.index:
+        check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _matrix(t: torch.Tensor, name: str, shape=None, dtypes=None) -> torch.Tensor:
+    """t, if it is a 2-D tensor with unit column stride and a row pitch that covers its columns."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be a 2-D tensor" + (f" of shape {shape}" if shape else ""))
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}")
+    if (t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return t
+
+
+def _pitch(t: torch.Tensor) -> int:
+    # the stride of a single row says nothing (torch may give any value): its
+    # columns, rounded up to a 16-byte pitch
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _blocks8(codes: torch.Tensor, scales: torch.Tensor, block_rows: int, what: str):
+    """(rows, K) of e4m3 codes [rows, K] with fp32 scales [ceil(rows / block_rows), K / 128]."""
+    if codes.dim() != 2 or codes.dtype != torch.float8_e4m3fn or not codes.is_contiguous():
+        raise ValueError(f"{what}: codes must be contiguous float8_e4m3fn [rows, K]")
+    rows, K = codes.shape
+    if block_rows not in (1, 128):
+        raise ValueError(f"{what}: block_rows must be 1 or 128")
+    if K % 128:
+        raise ValueError(f"{what}: K={K} is not a multiple of 128")
+    shape = (-(-rows // block_rows), K // 128)
+    if tuple(scales.shape) != shape or scales.dtype != torch.float32 or not scales.is_contiguous():
+        raise ValueError(f"{what}: scales must be contiguous fp32 of shape {shape}")
+    return rows, K
+
+
+def _header(workspace: Optional[torch.Tensor], dev: torch.device) -> torch.Tensor:
+    if workspace is None or workspace.numel() * workspace.element_size() < _HEADER_BYTES:
+        return torch.empty(_HEADER_BYTES, dtype=torch.uint8, device=dev)
+    return workspace
+
+
+def pack8(X: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = None,
+          scales: Optional[torch.Tensor] = None):
+    """e4m3 codes of X (fp16, bf16 or fp32 [rows, K]) with one power-of-two
+    scale per 128 columns of a row (block_rows=1: activations, and their
+    checkpoints) or per 128 x 128 block (block_rows=128: weights).
+
+    Returns (codes float8_e4m3fn [rows, K], scales fp32
+    [ceil(rows / block_rows), K / 128]); X ~= codes * scales. Output tensors of
+    those shapes may be passed in to be filled. Values that are not finite
+    become NaN codes and leave their block's scale alone.
+    """
+    lib = _lib.load()
+    dev = _require_cuda(X, codes, scales)
+    _matrix(X, "X", dtypes=_DT8)
+    rows, K = X.shape
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    if codes is None:
+        codes = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=dev)
+    if scales is None:
+        scales = torch.empty((-(-rows // block_rows), K // 128), dtype=torch.float32, device=dev)
+    if tuple(codes.shape) != (rows, K):
+        raise ValueError(f"codes must have shape {(rows, K)}")
+    if K % 128 == 0:        # the library refuses other K by name
+        _blocks8(codes, scales, block_rows, "pack8")
+    _call(dev, lib.rb_pack8, X.data_ptr(), _DT8[X.dtype], _pitch(X), rows, K, block_rows, codes.data_ptr(),
+          scales.data_ptr())
+    return codes, scales
+
+
+def unpack8(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torch.float16,
+            X: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """X = codes * scales in `dtype` (fp16, bf16 or fp32; X's own where X is given)."""
+    lib = _lib.load()
+    dev = _require_cuda(codes, scales, X)
+    rows, K = _blocks8(codes, scales, block_rows, "unpack8")
+    if X is None:
+        if dtype not in _DT8:
+            raise ValueError(f"dtype {dtype}")
+        X = torch.empty((rows, K), dtype=dtype, device=dev)
+    _matrix(X, "X", (rows, K), _DT8)
+    _call(dev, lib.rb_unpack8, codes.data_ptr(), scales.data_ptr(), rows, K, block_rows, X.data_ptr(), _DT8[X.dtype],
+          _pitch(X))
+    return X
+
+
+def gemm8(w: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor,
+          Y: Optional[torch.Tensor] = None, y_dtype: torch.dtype = torch.float16,
+          workspace: Optional[torch.Tensor] = None, check_device: bool = False) -> torch.Tensor:
+    """Y[t] = W x[t] from 8-bit blocks: w, w_scales = pack8(W, block_rows=128),
+    x, x_scales = pack8(X). Any number of tokens; any fp32 scales. With
+    check_device=True the call waits for the stream and raises if the kernel
+    recorded a failure (rb_gemm_check)."""
+    lib = _lib.load()
+    dev = _require_cuda(w, w_scales, x, x_scales, Y, workspace)
+    M, K = _blocks8(w, w_scales, 128, "w")
+    T, Kx = _blocks8(x, x_scales, 1, "x")
+    if Kx != K:
+        raise ValueError("w and x disagree on K")
+    if Y is None:
+        if y_dtype not in _DT8:
+            raise ValueError(f"y_dtype {y_dtype}")
+        Y = torch.empty((T, M), dtype=y_dtype, device=dev)
+    _matrix(Y, "Y", (T, M), _DT8)
+    workspace = _header(workspace, dev)
+    _call(dev, lib.rb_gemm8, w.data_ptr(), w_scales.data_ptr(), x.data_ptr(), x_scales.data_ptr(), M, K, T, Y.data_ptr(),
+          _DT8[Y.dtype], max(_pitch(Y), M), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if check_device:
+        _call(dev, lib.rb_gemm_check, workspace.data_ptr())
+    return Y
+
+
+def gemm_wgrad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, add: Optional[torch.Tensor] = None,
+               dW: Optional[torch.Tensor] = None, dw_dtype: torch.dtype = torch.float32,
+               workspace: Optional[torch.Tensor] = None, check_device: bool = False) -> torch.Tensor:
+    """Weight gradient from an 8-bit checkpoint of the layer's input:
+    dW = add + dY^T X with dY fp16 or bf16 [T, M] and codes, scales = pack8(X).
+
+    `add` (of dW's type and row pitch) may be dW itself: gradients summed over
+    micro-batches. The products see X rounded to dY's type (exact for a
+    checkpoint of a tensor of that type), sums are fp32 and dW is rounded once.
+    """
+    lib = _lib.load()
+    dev = _require_cuda(dY, codes, scales, add, dW, workspace)
+    T, K = _blocks8(codes, scales, 1, "checkpoint")
+    _matrix(dY, "dY", dtypes=(torch.float16, torch.bfloat16))
+    if dY.shape[0] != T:
+        raise ValueError("dY and the checkpoint disagree on the number of tokens")
+    M = dY.shape[1]
+    if dW is None:
+        dt = dw_dtype if add is None else add.dtype
+        if dt not in _DT8:
+            raise ValueError(f"dw_dtype {dt}")
+        dW = torch.empty((M, K), dtype=dt, device=dev)
+    _matrix(dW, "dW", (M, K), _DT8)
+    if add is not None:
+        _matrix(add, "add", (M, K), (dW.dtype,))
+        if _pitch(add) != _pitch(dW):
+            raise ValueError("add must have dW's row pitch")
+    workspace = _header(workspace, dev)
+    _call(dev, lib.rb_gemm_wgrad, dY.data_ptr(), _DT8[dY.dtype], _pitch(dY), M, codes.data_ptr(), scales.data_ptr(), K, T,
+          0 if add is None else add.data_ptr(), dW.data_ptr(), _DT8[dW.dtype], _pitch(dW), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    if check_device:
+        _call(dev, lib.rb_gemm_check, workspace.data_ptr())
+    return dW
+
+
+def gemm_dgrad(planes: torch.Tensor, alpha: torch.Tensor, dY: torch.Tensor, K: int, group: int = 0,
+               dX: Optional[torch.Tensor] = None, dx_dtype: torch.dtype = torch.float16,
+               workspace: Optional[torch.Tensor] = None, check_device: bool = False) -> torch.Tensor:
+    """Gradient of gemm() with respect to its input: dX = dY W^ with
+    W^ = sum_k alpha_k (.) B_k taken straight from the planes, dY fp16 or bf16
+    [T, M]. K is the layer's input width (sliced planes are padded to 512
+    columns, so they do not say it)."""
+    lib = _lib.load()
+    dev = _require_cuda(planes, alpha, dY, dX, workspace)
+    N, M, order = _planes_geometry(planes, K)
+    if planes.dtype != torch.int32 or not planes.is_contiguous():
+        raise ValueError("planes must be contiguous int32")
+    G = K if group == 0 else group
+    if alpha.dtype not in _DT or tuple(alpha.shape) != (N, M, K // G) or not alpha.is_contiguous():
+        raise ValueError(f"alpha must be contiguous fp16 or fp32 of shape {(N, M, K // G)}")
+    _matrix(dY, "dY", dtypes=(torch.float16, torch.bfloat16))
+    if dY.shape[1] != M:
+        raise ValueError("dY must have M columns")
+    T = dY.shape[0]
+    if dX is None:
+        if dx_dtype not in _DT8:
+            raise ValueError(f"dx_dtype {dx_dtype}")
+        dX = torch.empty((T, K), dtype=dx_dtype, device=dev)
+    _matrix(dX, "dX", (T, K), _DT8)
+    workspace = _header(workspace, dev)
+    _call(dev, lib.rb_gemm_dgrad, planes.data_ptr(), alpha.data_ptr(), _DT[alpha.dtype], layout(M, K, N, group, order),
+          dY.data_ptr(), _DT8[dY.dtype], _pitch(dY), T, dX.data_ptr(), _DT8[dX.dtype], _pitch(dX), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    if check_device:
+        _call(dev, lib.rb_gemm_check, workspace.data_ptr())
+    return dX

@@ -68,6 +68,32 @@ static size_t dtype_size(rb_dtype d) { return d == RB_F16 ? 2 : 4; }
 
 static bool valid_dtype(rb_dtype d) { return d == RB_F16 || d == RB_F32; }
 
+// dtypes of the 8-bit block and gradient calls
+static bool valid_dtype8(rb_dtype d) { return d == RB_F32 || d == RB_F16 || d == RB_BF16; }
+static size_t dtype8_size(rb_dtype d) { return d == RB_F32 ? 4 : 2; }
+
+static rb_status check_blocks8(int64_t rows, int64_t K, const char* what) {
+    if (rows <= 0 || K <= 0)
+        return fail(RB_ERR_INVALID_ARG, "%s and K must be positive (%lld, %lld)", what, (long long)rows, (long long)K);
+    if (K % 128 != 0) return fail(RB_ERR_UNSUPPORTED, "K=%lld is not a multiple of 128", (long long)K);
+    if (K > (1ll << 31) || rows >= (1ll << 31) / (K / 128))
+        return fail(RB_ERR_UNSUPPORTED, "%s=%lld x K=%lld: 2^31 blocks of 128 or more", what, (long long)rows, (long long)K);
+    return RB_OK;
+}
+
+static rb_status check_header(const void* workspace, size_t ws_bytes) {
+    if (!workspace || ws_bytes < GEMM_HEADER_BYTES || !aligned16(workspace))
+        return fail(RB_ERR_WORKSPACE, "workspace needs %zu bytes (16-byte aligned), got %zu", (size_t)GEMM_HEADER_BYTES,
+                    ws_bytes);
+    return RB_OK;
+}
+
+static rb_status launched(cudaError_t e, const char* who) {
+    if (e == cudaErrorNotSupported) return fail(RB_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    if (e != cudaSuccess) return cuda_fail(e, who);
+    return RB_OK;
+}
+
 static size_t gv_ws_bytes(const GvPlan& pl) {
     if (pl.counters == 0 && pl.partials == 0) return GV_HEADER_BYTES;
     return GV_HEADER_BYTES + GV_CTR_ZONE_BYTES + pl.partials * 4;
@@ -456,6 +482,113 @@ rb_status rb_gemm_reconstruct(const uint32_t* planes, const void* alpha, rb_dtyp
     if (e == cudaErrorNotSupported) return fail(RB_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     if (e != cudaSuccess) return cuda_fail(e, "rb_gemm_reconstruct launch");
     return RB_OK;
+}
+
+rb_status rb_pack8(const void* X, rb_dtype x_dtype, int64_t ldx, int64_t rows, int64_t K, int32_t block_rows,
+                   uint8_t* codes, float* scales, void* stream) {
+    g_last_error.clear();
+    rb_status st = check_blocks8(rows, K, "rows");
+    if (st != RB_OK) return st;
+    if (block_rows != 1 && block_rows != 128) return fail(RB_ERR_UNSUPPORTED, "block_rows=%d (1 or 128)", block_rows);
+    if (!X || !codes || !scales) return fail(RB_ERR_INVALID_ARG, "null X, codes or scales");
+    if (!valid_dtype8(x_dtype)) return fail(RB_ERR_INVALID_ARG, "bad x_dtype %d", (int)x_dtype);
+    if (ldx < K) return fail(RB_ERR_INVALID_ARG, "ldx=%lld < K=%lld", (long long)ldx, (long long)K);
+    if (!aligned16(X) || (ldx * dtype8_size(x_dtype)) % 16 != 0)
+        return fail(RB_ERR_ALIGNMENT, "X and its row pitch must be 16-byte aligned");
+    if (!aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u))
+        return fail(RB_ERR_ALIGNMENT, "codes must be 16-byte aligned, scales 4-byte aligned");
+    return launched(launch_pack8(X, x_dtype, ldx, rows, K, block_rows, codes, scales, static_cast<cudaStream_t>(stream)),
+                    "rb_pack8 launch");
+}
+
+rb_status rb_unpack8(const uint8_t* codes, const float* scales, int64_t rows, int64_t K, int32_t block_rows, void* X,
+                     rb_dtype x_dtype, int64_t ldx, void* stream) {
+    g_last_error.clear();
+    rb_status st = check_blocks8(rows, K, "rows");
+    if (st != RB_OK) return st;
+    if (block_rows != 1 && block_rows != 128) return fail(RB_ERR_UNSUPPORTED, "block_rows=%d (1 or 128)", block_rows);
+    if (!X || !codes || !scales) return fail(RB_ERR_INVALID_ARG, "null X, codes or scales");
+    if (!valid_dtype8(x_dtype)) return fail(RB_ERR_INVALID_ARG, "bad x_dtype %d", (int)x_dtype);
+    if (ldx < K) return fail(RB_ERR_INVALID_ARG, "ldx=%lld < K=%lld", (long long)ldx, (long long)K);
+    if (!aligned16(X) || (ldx * dtype8_size(x_dtype)) % 16 != 0)
+        return fail(RB_ERR_ALIGNMENT, "X and its row pitch must be 16-byte aligned");
+    if (!aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u))
+        return fail(RB_ERR_ALIGNMENT, "codes must be 16-byte aligned, scales 4-byte aligned");
+    return launched(launch_unpack8(codes, scales, rows, K, block_rows, X, x_dtype, ldx, static_cast<cudaStream_t>(stream)),
+                    "rb_unpack8 launch");
+}
+
+rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t* x, const float* x_scales, int64_t M, int64_t K,
+                   int32_t T, void* Y, rb_dtype y_dtype, int64_t ldy, void* workspace, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    rb_status st = check_blocks8(M, K, "M");
+    if (st != RB_OK) return st;
+    if (!w || !w_scales || !x || !x_scales || !Y) return fail(RB_ERR_INVALID_ARG, "null w, x, their scales or Y");
+    if (!valid_dtype8(y_dtype)) return fail(RB_ERR_INVALID_ARG, "bad y_dtype %d", (int)y_dtype);
+    if (T < 1 || T > (1 << 22)) return fail(RB_ERR_UNSUPPORTED, "T=%d outside 1..2^22", T);
+    if ((st = check_blocks8(T, K, "T")) != RB_OK) return st;
+    if (ldy < M) return fail(RB_ERR_INVALID_ARG, "ldy=%lld < M=%lld", (long long)ldy, (long long)M);
+    if (!aligned16(w) || !aligned16(x)) return fail(RB_ERR_ALIGNMENT, "w and x must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(w_scales) & 3u) || (reinterpret_cast<uintptr_t>(x_scales) & 3u))
+        return fail(RB_ERR_ALIGNMENT, "scales must be 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(Y) & (dtype8_size(y_dtype) - 1)) return fail(RB_ERR_ALIGNMENT, "Y misaligned");
+    if ((st = check_header(workspace, ws_bytes)) != RB_OK) return st;
+    if (static_cast<double>((T + 127) / 128) * static_cast<double>((M + 127) / 128) >= 268435456.0)
+        return fail(RB_ERR_UNSUPPORTED, "T=%d x M=%lld: 2^28 tiles or more", T, (long long)M);
+    return launched(launch_gemm8(w, w_scales, x, x_scales, M, K, T, Y, y_dtype, ldy, static_cast<uint32_t*>(workspace) + 1,
+                                 static_cast<cudaStream_t>(stream)),
+                    "rb_gemm8 launch");
+}
+
+// what rb_gemm_wgrad and rb_gemm_dgrad share: dY, the output and the header
+static rb_status check_gradient(const void* dY, rb_dtype dy_dtype, int64_t ldd, int64_t M, int64_t K, int32_t T,
+                                const void* out, rb_dtype out_dtype, int64_t ldo, const void* workspace, size_t ws_bytes) {
+    if (dy_dtype != RB_F16 && dy_dtype != RB_BF16)
+        return fail(dy_dtype == RB_F32 ? RB_ERR_UNSUPPORTED : RB_ERR_INVALID_ARG, "dY must be fp16 or bf16 (dy_dtype %d)",
+                    (int)dy_dtype);
+    if (!valid_dtype8(out_dtype)) return fail(RB_ERR_INVALID_ARG, "bad output dtype %d", (int)out_dtype);
+    if (T < 1 || T > (1 << 22)) return fail(RB_ERR_UNSUPPORTED, "T=%d outside 1..2^22", T);
+    if (ldd < M || ldo < K) return fail(RB_ERR_INVALID_ARG, "the row pitch of dY is below M, or the output's below K");
+    if (!aligned16(dY) || (ldd * 2) % 16 != 0)
+        return fail(RB_ERR_ALIGNMENT, "dY and its row pitch must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(out) & (dtype8_size(out_dtype) - 1)) return fail(RB_ERR_ALIGNMENT, "output misaligned");
+    return check_header(workspace, ws_bytes);
+}
+
+rb_status rb_gemm_wgrad(const void* dY, rb_dtype dy_dtype, int64_t ldd, int64_t M, const uint8_t* codes,
+                        const float* scales, int64_t K, int32_t T, const void* add, void* dW, rb_dtype dw_dtype,
+                        int64_t ldw, void* workspace, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    rb_status st = check_blocks8(M, K, "M");
+    if (st != RB_OK) return st;
+    if (!dY || !codes || !scales || !dW) return fail(RB_ERR_INVALID_ARG, "null dY, codes, scales or dW");
+    if ((st = check_gradient(dY, dy_dtype, ldd, M, K, T, dW, dw_dtype, ldw, workspace, ws_bytes)) != RB_OK) return st;
+    if ((st = check_blocks8(T, K, "T")) != RB_OK) return st;
+    if (!aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u))
+        return fail(RB_ERR_ALIGNMENT, "codes must be 16-byte aligned, scales 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(add) & (dtype8_size(dw_dtype) - 1)) return fail(RB_ERR_ALIGNMENT, "add misaligned");
+    return launched(launch_gemm_wgrad(dY, dy_dtype == RB_BF16, ldd, M, codes, scales, K, T, add, dW, dw_dtype, ldw,
+                                      static_cast<uint32_t*>(workspace) + 1, static_cast<cudaStream_t>(stream)),
+                    "rb_gemm_wgrad launch");
+}
+
+rb_status rb_gemm_dgrad(const uint32_t* planes, const void* alpha, rb_dtype alpha_dtype, rb_layout L, const void* dY,
+                        rb_dtype dy_dtype, int64_t ldd, int32_t T, void* dX, rb_dtype dx_dtype, int64_t ldx,
+                        void* workspace, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    rb_status st = check_layout(L);
+    if (st != RB_OK) return st;
+    if (!planes || !alpha || !dY || !dX) return fail(RB_ERR_INVALID_ARG, "null planes, alpha, dY or dX");
+    if (!valid_dtype(alpha_dtype)) return fail(RB_ERR_INVALID_ARG, "bad alpha_dtype %d", (int)alpha_dtype);
+    if (L.n_paths > 4) return fail(RB_ERR_UNSUPPORTED, "rb_gemm_dgrad supports 1..4 paths");
+    if ((st = check_gradient(dY, dy_dtype, ldd, L.M, L.K, T, dX, dx_dtype, ldx, workspace, ws_bytes)) != RB_OK) return st;
+    if (!aligned16(planes)) return fail(RB_ERR_ALIGNMENT, "planes must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(alpha) & (dtype_size(alpha_dtype) - 1))
+        return fail(RB_ERR_ALIGNMENT, "alpha misaligned for its dtype");
+    return launched(launch_gemm_dgrad(planes, alpha, alpha_dtype == RB_F16, L.M, L.K, L.n_paths, L.group,
+                                      L.order == RB_SLICED, dY, dy_dtype == RB_BF16, ldd, T, dX, dx_dtype, ldx,
+                                      static_cast<uint32_t*>(workspace) + 1, static_cast<cudaStream_t>(stream)),
+                    "rb_gemm_dgrad launch");
 }
 
 // Wait for `stream`, then read word 1 (the error flags) of a workspace header.

@@ -1,0 +1,543 @@
+// Backward pass of the layer on the tcgen05 tensor cores:
+//
+//   rb_gemm_dgrad   dX[t][j] = sum_i dY[t][i] W^[i][j],  W^ = sum_k alpha_k (.) B_k
+//   rb_gemm_wgrad   dW[m][j] = add[m][j] + sum_t dY[t][m] s[t][j / 128] c[t][j]
+//
+// Both are products P[n][j] = sum_r B[n][r] A[r][j] in which one operand
+// comes from HBM in a compressed form (sign planes and scales, or e4m3 codes
+// and scales) whose rows run along the columns j, and the other is dY in 16
+// bits. A 128-column tile of the compressed operand is expanded, 64 rows r at
+// a time, into shared memory as the MMA's A (columns j = MMA rows, stored
+// "M-major": 64 columns of one r per 128-byte swizzled row), so neither a
+// transposed nor an expanded copy of it ever reaches HBM. dY tiles arrive by TMA:
+// K-major for dgrad (a row of dY runs along r = i), N-major for wgrad (it
+// runs along n = m).
+//
+// Roles (448 threads): warps 0-3 epilogue, 4-11 expansion, 12 TMA, 13 MMAs.
+// A CTA walks its tiles with two accumulators, so the epilogue of a tile
+// overlaps the next tile's MMAs. Few tiles: a cluster of CTAs shares a
+// tile, each takes part of the rows r, and the sums meet in distributed
+// shared memory in rank order.
+//
+// Rounding: dgrad's operand W^[i][j] is the exact sum of the scales (to fp32)
+// rounded once to dY's 16-bit type; wgrad's operand s c is exact in that type
+// for scales that are powers of two in its range, as rb_pack8 writes them,
+// and rounded to it otherwise. Products are exact, sums fp32.
+#include "rb_tc.cuh"
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+namespace rb {
+namespace {
+
+using namespace tc;
+
+constexpr int EPI_WARPS = 4, EXP_WARP0 = 4, EXP_WARPS = 8, TMA_WARP = 12, MMA_WARP = 13;
+constexpr int THREADS = 448;
+constexpr int BR = 64;                          // rows r per stage
+constexpr uint32_t A_BYTES = 128 * BR * 2;      // two chunks of [64 r][64 j]
+constexpr uint32_t CHUNK = 64 * BR * 2;         // 8 KB
+constexpr int MAX_STAGES = 8;
+enum : int { DGRAD = 0, WGRAD = 1 };
+
+struct BwArgs {
+    uint32_t* err;
+    const uint32_t* planes;     // dgrad
+    const void* alpha;
+    const uint8_t* codes;       // wgrad
+    const float* scales;
+    const void* add;            // wgrad, may be null
+    void* out;
+    int64_t R, N, J, ldo;       // contraction, output rows, output columns (K)
+    int j_tiles, n_tiles;
+    int stages;
+    int out_dt;
+    bool sliced, alpha_f16, g128;
+};
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t local, uint32_t rank) {
+    uint32_t addr;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(local), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+// Descriptor of an M-major (N-major) tile in the 128-byte swizzle layout:
+// 64 columns of one row r per 128 bytes, 8 rows per 1024-byte atom (stride
+// offset 1024), the next 64 columns one chunk on (leading offset CHUNK).
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(CHUNK >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+
+// fp32 accumulator, A and B both fp16 or both bf16, A M-major, B K- or N-major
+__host__ __device__ constexpr uint32_t idesc_bw(int n, bool bf16, bool b_mn) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (1u << 15) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);
+}
+
+// two floats in the 16-bit type of dY
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// What one expansion thread holds of one stage: row r, 32 columns.
+template <int MODE, int NP>
+struct Unit;
+
+template <int NP>
+struct Unit<DGRAD, NP> {
+    uint32_t w[NP];
+    float al[NP];
+    __device__ __forceinline__ void load(const BwArgs& a, int64_t r, int64_t j) {
+        const int64_t i = r < a.R ? r : a.R - 1;
+        const int64_t W32 = a.J >> 5, S = (a.J + 511) >> 9, gpr = a.J >> 7, word = j >> 5;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            w[p] = __ldg(a.sliced ? a.planes + ((p * S + (word >> 4)) * a.R + i) * 16 + (word & 15)
+                                  : a.planes + (p * a.R + i) * W32 + word);
+            const int64_t ai = a.g128 ? (p * a.R + i) * gpr + (j >> 7) : p * a.R + i;
+            const float v = a.alpha_f16 ? __half2float(__ldg(static_cast<const __half*>(a.alpha) + ai))
+                                        : __ldg(static_cast<const float*>(a.alpha) + ai);
+            al[p] = r < a.R ? v : 0.0f;      // rows past the last: zeros
+        }
+    }
+    // the 32 weights sum_p +-alpha_p: path 0 gives the sign, the paths that
+    // agree or disagree with it choose one of 2^(NP-1) magnitudes
+    template <bool BF16>
+    __device__ __forceinline__ void expand(uint32_t (&h)[16]) const {
+        constexpr int NM = 1 << (NP - 1);
+        uint32_t mag[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            float v = al[0];
+#pragma unroll
+            for (int p = 1; p < NP; ++p) v += (m >> (p - 1)) & 1 ? al[p] : -al[p];
+            mag[m] = pack2<BF16>(v, v);
+        }
+        uint32_t s[NP][8];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const uint32_t x = p == 0 ? w[0] : ~(w[0] ^ w[p]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[p][k] = x << (7 - k);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            // columns 2i and 2i+1: bit 8b + 2m (+ 1) is the top bit of byte b of s[2m (+ 1)]
+            const int m = i & 3, b = i >> 2;
+            const uint32_t lo = 8u | b, hi = 8u | (4u + b);
+            uint32_t v[NM];
+#pragma unroll
+            for (int k = 0; k < NM; ++k) v[k] = mag[k];
+#pragma unroll
+            for (int p = 1; p < NP; ++p) {
+                const uint32_t mask = prmt(s[p][2 * m], s[p][2 * m + 1], lo | (lo << 4) | (hi << 8) | (hi << 12));
+#pragma unroll
+                for (int k = 0; k < (NM >> p); ++k) v[k] = (mask & v[2 * k + 1]) | (~mask & v[2 * k]);
+            }
+            const uint32_t sgn = prmt(s[0][2 * m], s[0][2 * m + 1], (lo << 4) | (hi << 12));
+            h[i] = v[0] ^ (~sgn & 0x80008000u);
+        }
+    }
+};
+
+template <int NP>
+struct Unit<WGRAD, NP> {
+    uint4 c0, c1;
+    float s;
+    __device__ __forceinline__ void load(const BwArgs& a, int64_t r, int64_t j) {
+        if (r < a.R) {
+            const uint4* p = reinterpret_cast<const uint4*>(a.codes + r * a.J + j);
+            c0 = __ldg(p);
+            c1 = __ldg(p + 1);
+            s = __ldg(a.scales + r * (a.J >> 7) + (j >> 7));
+        } else {
+            c0 = c1 = make_uint4(0u, 0u, 0u, 0u);
+            s = 0.0f;
+        }
+    }
+    template <bool BF16>
+    __device__ __forceinline__ void expand(uint32_t (&h)[16]) const {
+        const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
+                "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+                : "=r"(h[2 * i]), "=r"(h[2 * i + 1])
+                : "r"(c[i]));
+        }
+        // a scale that fp16 holds exactly: one fp16 product rounds s c once
+        const __half sh = __float2half_rn(s);
+        if (!BF16 && __half2float(sh) == s) {
+            const __half2 s2 = __half2half2(sh);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), s2);
+                h[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+                h[i] = pack2<BF16>(f.x * s, f.y * s);
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ float load_out(const void* p, int dt, int64_t i) {
+    if (dt == B8_F32) return static_cast<const float*>(p)[i];
+    if (dt == B8_F16) return __half2float(static_cast<const __half*>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_out(void* p, int dt, int64_t i, float v) {
+    if (dt == B8_F32) static_cast<float*>(p)[i] = v;
+    else if (dt == B8_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+template <int MODE, int NP, int BN, bool BF16, bool SPLIT>
+__global__ void __launch_bounds__(THREADS, 1)
+gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, BwArgs a) {
+    constexpr uint32_t B_BYTES = BN * BR * 2, STAGE = A_BYTES + B_BYTES;
+    constexpr uint32_t TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    constexpr int PD = 3;                    // stages of compressed operand held in registers ahead of use
+    extern __shared__ __align__(1024) unsigned char dsm[];
+    __shared__ __align__(8) uint64_t bars[3 * MAX_STAGES + 4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ uint32_t abort_word;
+    volatile uint32_t* abort_flag = &abort_word;
+    const uint32_t tiles = (smem_addr(dsm) + 1023u) & ~1023u;
+    const int stages = a.stages;
+    auto a_tile = [&](int s) { return tiles + static_cast<uint32_t>(s) * STAGE; };
+    auto b_tile = [&](int s) { return tiles + static_cast<uint32_t>(s) * STAGE + A_BYTES; };
+    const uint32_t bar0 = smem_addr(bars);
+    auto full_b = [&](int s) { return bar0 + 8u * s; };
+    auto full_a = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (3 * MAX_STAGES + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (3 * MAX_STAGES + 2 + b); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t* err = a.err;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;      // flags are raised only by waits that ran out
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full_b(s), 1);
+            mbar_init(full_a(s), EXP_WARPS);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full(b), 1);
+            mbar_init(acc_empty(b), EPI_WARPS);
+        }
+        abort_word = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == MMA_WARP) tmem_alloc(smem_addr(&tmem_slot), TMEM_COLS);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    const uint32_t rank = SPLIT ? cluster_rank() : 0u, size = SPLIT ? cluster_size() : 1u;
+    const int64_t nr = (a.R + BR - 1) / BR;
+    const int r_lo = static_cast<int>(nr * rank / size), r_hi = static_cast<int>(nr * (rank + 1) / size);
+    const int units = a.j_tiles * a.n_tiles;
+    const int u0 = SPLIT ? blockIdx.x / size : blockIdx.x;
+    const int u_step = SPLIT ? units : gridDim.x;
+
+    if (warp == TMA_WARP) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int u = u0; u < units && ok; u += u_step) {
+                const int nt = u / a.j_tiles;
+                for (int rb = r_lo; rb < r_hi; ++rb, ++it) {
+                    const int s = it % stages;
+                    if (!mbar_wait(empty_bar(s), (static_cast<uint32_t>(it / stages) & 1u) ^ 1u, abort_flag, err, 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(full_b(s), B_BYTES);
+                    if constexpr (MODE == DGRAD) {
+                        tma_load_2d(b_tile(s), &dmap, rb * BR, nt * BN, full_b(s));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < BN / 64; ++c)
+                            tma_load_2d(b_tile(s) + c * CHUNK, &dmap, nt * BN + c * 64, rb * BR, full_b(s));
+                    }
+                }
+            }
+            // after an abort the loads in flight land before the CTA gives up its shared memory
+            if (*abort_flag)
+                for (int i = it - 1; i >= 0 && i >= it - stages; --i)
+                    mbar_drain(full_b(i % stages), static_cast<uint32_t>(i / stages) & 1u);
+        }
+    } else if (warp == MMA_WARP) {
+        constexpr uint32_t idesc = idesc_bw(BN, BF16, MODE == WGRAD);
+        int it = 0, tile = 0;
+        bool ok = true;
+        for (int u = u0; u < units && ok; u += u_step, ++tile) {
+            const int b = tile & 1;
+            ok = __all_sync(FULL_MASK, mbar_wait(acc_empty(b), (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u, abort_flag, err, 2u));
+            for (int rb = r_lo; rb < r_hi && ok; ++rb, ++it) {
+                const int s = it % stages;
+                const uint32_t ph = static_cast<uint32_t>(it / stages) & 1u;
+                if (!__all_sync(FULL_MASK, mbar_wait(full_b(s), ph, abort_flag, err, 2u) &&
+                                               mbar_wait(full_a(s), ph, abort_flag, err, 2u))) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+#pragma unroll
+                for (int kk = 0; kk < BR / 16; ++kk) {
+                    // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
+                    const uint64_t bd = MODE == DGRAD ? smem_desc(b_tile(s)) + 2u * kk : smem_desc_mn(b_tile(s) + 2048u * kk);
+                    umma_f16_elect(tmem + static_cast<uint32_t>(b * BN), smem_desc_mn(a_tile(s) + 2048u * kk), bd, idesc,
+                                   (rb > r_lo || kk > 0) ? 1u : 0u);
+                }
+                umma_commit_elect(empty_bar(s));
+            }
+            // also after an abort: the teardown waits for it
+            umma_commit_elect(acc_full(b));
+        }
+        // every MMA issued has completed before the tensor memory is given up
+        if (!ok)
+            for (int i = tile - 1; i >= 0 && i >= tile - 2; --i) mbar_drain(acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u);
+    } else if (warp >= EXP_WARP0) {
+        const int e = warp - EXP_WARP0, wd = e & 3;
+        const int row = (e >> 2) * 32 + lane;                // row r within the stage
+        const uint32_t at = static_cast<uint32_t>(wd >> 1) * CHUNK + static_cast<uint32_t>(row) * 128u;
+        const uint32_t sw = static_cast<uint32_t>(row & 7), c0 = static_cast<uint32_t>(wd & 1) * 4u;
+        int it = 0;
+        bool ok = true;
+        for (int u = u0; u < units && ok; u += u_step) {
+            const int64_t j = static_cast<int64_t>(u % a.j_tiles) * 128 + wd * 32;
+            Unit<MODE, NP> ring[PD];
+#pragma unroll
+            for (int i = 0; i < PD; ++i)
+                if (r_lo + i < r_hi) ring[i].load(a, static_cast<int64_t>(r_lo + i) * BR + row, j);
+            for (int rb0 = r_lo; rb0 < r_hi && ok; rb0 += PD) {
+#pragma unroll
+                for (int i = 0; i < PD; ++i) {
+                    const int rb = rb0 + i;
+                    if (rb < r_hi && ok) {
+                        const int s = it % stages;
+                        uint32_t h[16];
+                        ring[i].template expand<BF16>(h);
+                        if (rb + PD < r_hi) ring[i].load(a, static_cast<int64_t>(rb + PD) * BR + row, j);
+                        if (!__all_sync(FULL_MASK, mbar_wait(empty_bar(s), (static_cast<uint32_t>(it / stages) & 1u) ^ 1u,
+                                                             abort_flag, err, 4u))) {
+                            ok = false;
+                        } else {
+                            const uint32_t base = a_tile(s) + at;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                sts128(base + (((c0 + c) ^ sw) << 4), h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+                            fence_proxy_async_smem();   // make the generic-proxy stores visible to the tensor core
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(full_a(s));
+                            ++it;
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+        int tile = 0;
+        for (int u = u0; u < units; u += u_step, ++tile) {
+            const int b = tile & 1;
+            const int64_t j = static_cast<int64_t>(u % a.j_tiles) * 128 + warp * 32 + lane;
+            const int64_t n0 = static_cast<int64_t>(u / a.j_tiles) * BN;
+            if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(tile >> 1) & 1u, abort_flag, err, 8u)) ||
+                *abort_flag)
+                break;
+            fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < BN; c0 += 32) {
+                uint32_t v[32];
+                tmem_load<32>(tmem + lanes + static_cast<uint32_t>(b * BN + c0), v);
+                if constexpr (SPLIT) {
+                    float* buf = reinterpret_cast<float*>(dsm + (tiles - smem_addr(dsm))) + c0 * 128 + warp * 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) buf[i * 128] = __uint_as_float(v[i]);
+                } else {
+                    const int left = static_cast<int>(min(static_cast<int64_t>(32), a.N - n0 - c0));
+                    if (MODE == WGRAD && a.add) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < left)
+                                v[i] = __float_as_uint(__uint_as_float(v[i]) + load_out(a.add, a.out_dt, (n0 + c0 + i) * a.ldo + j));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < left) store_out(a.out, a.out_dt, (n0 + c0 + i) * a.ldo + j, __uint_as_float(v[i]));
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty(b));
+        }
+    }
+    __syncwarp();
+    fence_before();
+    if constexpr (SPLIT) {
+        cluster_sync();
+        // the CTAs of the cluster take the output rows in turn and add the ranks' sums in rank order
+        const int64_t j = static_cast<int64_t>(u0 % a.j_tiles) * 128 + (threadIdx.x & 127);
+        const int64_t n0 = static_cast<int64_t>(u0 / a.j_tiles) * BN;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(BN), a.N - n0));
+        if (*abort_flag == 0u && threadIdx.x < 384) {
+            for (int c = static_cast<int>(rank) * 3 + (threadIdx.x >> 7); c < rows; c += static_cast<int>(size) * 3) {
+                float v = 0.0f;
+                for (uint32_t k = 0; k < size; ++k) v += ld_cluster(tiles + static_cast<uint32_t>(c * 128 + (threadIdx.x & 127)) * 4u, k);
+                const int64_t o = (n0 + c) * a.ldo + j;
+                if (MODE == WGRAD && a.add) v += load_out(a.add, a.out_dt, o);
+                store_out(a.out, a.out_dt, o, v);
+            }
+        }
+        cluster_sync();      // no CTA leaves while another reads its sums
+    } else {
+        __syncthreads();
+    }
+    fence_after();
+    if (warp == MMA_WARP) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+template <int MODE, int NP, int BN, bool BF16, bool SPLIT>
+cudaError_t launch(const CUtensorMap& m, BwArgs& a, int split, cudaStream_t s) {
+    constexpr size_t stage = A_BYTES + BN * BR * 2;
+    a.stages = static_cast<int>(std::min<size_t>(MAX_STAGES, (200 * 1024) / stage));
+    // at least 120 KB, so that two CTAs never share an SM's tensor memory
+    const size_t smem = std::max<size_t>(1024 + std::max<size_t>(a.stages * stage, SPLIT ? BN * 512 : 0), 120 * 1024);
+    auto kern = gemm_bwd_kernel<MODE, NP, BN, BF16, SPLIT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int64_t units = static_cast<int64_t>(a.j_tiles) * a.n_tiles;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? units * split : std::min<int64_t>(units, device_sm_count())));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(split);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = SPLIT ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, m, a);
+}
+
+template <int MODE, int NP, int BN>
+cudaError_t launch_bn(const CUtensorMap& m, BwArgs& a, bool bf16, cudaStream_t s) {
+    a.n_tiles = static_cast<int>((a.N + BN - 1) / BN);
+    const int64_t units = static_cast<int64_t>(a.j_tiles) * a.n_tiles, nr = (a.R + BR - 1) / BR;
+    int split = 1;
+    while (split < 8 && units * (split + 1) <= device_sm_count() && split < nr) ++split;
+    if (split > 1)
+        return bf16 ? launch<MODE, NP, BN, true, true>(m, a, split, s) : launch<MODE, NP, BN, false, true>(m, a, split, s);
+    return bf16 ? launch<MODE, NP, BN, true, false>(m, a, 1, s) : launch<MODE, NP, BN, false, false>(m, a, 1, s);
+}
+
+template <int NP>
+cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, cudaStream_t s) {
+    CUtensorMap m;
+    const int bn = a.N <= 32 ? 32 : a.N <= 64 ? 64 : a.N <= 128 ? 128 : 256;
+    const cudaError_t e = make_x_map(&m, dY, a.R, a.N, ldd, bn);
+    if (e != cudaSuccess) return e;
+    switch (bn) {
+        case 32: return launch_bn<DGRAD, NP, 32>(m, a, bf16, s);
+        case 64: return launch_bn<DGRAD, NP, 64>(m, a, bf16, s);
+        case 128: return launch_bn<DGRAD, NP, 128>(m, a, bf16, s);
+        default: return launch_bn<DGRAD, NP, 256>(m, a, bf16, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_dgrad(const uint32_t* planes, const void* alpha, bool alpha_f16, int64_t M, int64_t K,
+                              int n_paths, int group, bool sliced, const void* dY, bool bf16, int64_t ldd, int T,
+                              void* dX, int dx_dt, int64_t ldx, uint32_t* err, cudaStream_t s) {
+    BwArgs a{};
+    a.err = err;
+    a.planes = planes;
+    a.alpha = alpha;
+    a.out = dX;
+    a.R = M;
+    a.N = T;
+    a.J = K;
+    a.ldo = ldx;
+    a.j_tiles = static_cast<int>(K / 128);
+    a.out_dt = dx_dt;
+    a.sliced = sliced;
+    a.alpha_f16 = alpha_f16;
+    a.g128 = group == 128;
+    switch (n_paths) {
+        case 1: return launch_dgrad_np<1>(a, dY, ldd, bf16, s);
+        case 2: return launch_dgrad_np<2>(a, dY, ldd, bf16, s);
+        case 3: return launch_dgrad_np<3>(a, dY, ldd, bf16, s);
+        case 4: return launch_dgrad_np<4>(a, dY, ldd, bf16, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M, const uint8_t* codes,
+                              const float* scales, int64_t K, int T, const void* add, void* dW, int dw_dt, int64_t ldw,
+                              uint32_t* err, cudaStream_t s) {
+    BwArgs a{};
+    a.err = err;
+    a.codes = codes;
+    a.scales = scales;
+    a.add = add;
+    a.out = dW;
+    a.R = T;
+    a.N = M;
+    a.J = K;
+    a.ldo = ldw;
+    a.j_tiles = static_cast<int>(K / 128);
+    a.out_dt = dw_dt;
+    CUtensorMap m;
+    const cudaError_t e = make_x_map(&m, dY, M, T, ldd, BR);      // boxes of 64 m x 64 t
+    if (e != cudaSuccess) return e;
+    if (M <= 64) return launch_bn<WGRAD, 1, 64>(m, a, bf16, s);
+    if (M <= 128) return launch_bn<WGRAD, 1, 128>(m, a, bf16, s);
+    return launch_bn<WGRAD, 1, 256>(m, a, bf16, s);
+}
+
+}  // namespace rb

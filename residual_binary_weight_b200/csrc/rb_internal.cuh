@@ -132,6 +132,23 @@ cudaError_t launch_dual_gemv(const uint32_t* planes, bool sliced, int64_t M, int
                              const float* g, const void* x, int64_t ldx, int T, void* y, bool y_f16, int64_t ldy,
                              void* workspace, const DualPlan& d, cudaStream_t s);
 
+// ------------------------------------------------- 8-bit blocks (e4m3 codes)
+// element types of rb_pack8, rb_unpack8, rb_gemm8, rb_gemm_wgrad and
+// rb_gemm_dgrad (the values of rb_dtype)
+enum : int { B8_F32 = 0, B8_F16 = 1, B8_BF16 = 2 };
+cudaError_t launch_pack8(const void* X, int dt, int64_t ldx, int64_t rows, int64_t K, int block_rows, uint8_t* codes,
+                         float* scales, cudaStream_t s);
+cudaError_t launch_unpack8(const uint8_t* codes, const float* scales, int64_t rows, int64_t K, int block_rows, void* X,
+                           int dt, int64_t ldx, cudaStream_t s);
+cudaError_t launch_gemm8(const uint8_t* W, const float* w_scales, const uint8_t* X, const float* x_scales, int64_t M,
+                         int64_t K, int T, void* Y, int y_dt, int64_t ldy, uint32_t* err, cudaStream_t s);
+cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M, const uint8_t* codes,
+                              const float* scales, int64_t K, int T, const void* add, void* dW, int dw_dt, int64_t ldw,
+                              uint32_t* err, cudaStream_t s);
+cudaError_t launch_gemm_dgrad(const uint32_t* planes, const void* alpha, bool alpha_f16, int64_t M, int64_t K,
+                              int n_paths, int group, bool sliced, const void* dY, bool bf16, int64_t ldd, int T,
+                              void* dX, int dx_dt, int64_t ldx, uint32_t* err, cudaStream_t s);
+
 int device_sm_count();
 
 // Device address of the static scratch array of rb_gemv_noalloc on the

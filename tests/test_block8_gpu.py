@@ -1,0 +1,516 @@
+"""8-bit blocks, the 8-bit product and the layer's gradients on the GPU,
+element by element against the fp64 oracle on the same inputs.
+
+Tolerances, from the arithmetic alone (D = sum of the magnitudes of a
+result's terms, u = 2^-24):
+  * codes, scales and unpacked values are exact;
+  * a sum of n products in fp32, in any order and with truncating adds, is
+    within n 2^-23 D;
+  * gemm8: the products of a block are exact in fp32, 128 per block: 2^-16 D,
+    then per block the factor (2 u) and one fused add (u), G of them, and the
+    ranks' sums of a split (8 u): (2^-16 + (G + 10) u) D;
+  * wgrad: T products exact in fp32, `add` one more term and one more add;
+  * dgrad: the operand's rounding eps / 2 (eps of dY's type) and that of its
+    scales' fp32 sum (3 u), then M products: (eps / 2 + 3 u + M 2^-23) D;
+  * in both, a magnitude in D counts at least as its type's smallest normal
+    value: the tensor core aligns the terms of a sum by the operands' exponent
+    fields, and a subnormal operand carries the smallest normal exponent, so
+    a term cuts sums off at 2^-23 of max(|a|, tiny) max(|b|, tiny) (with two
+    terms per sum: within 0.96 of 2^-23 of that, and within 0.94 of
+    2^-23 |a b| where no operand is subnormal; a single product is exact);
+  * the output's rounding eps / 2 of the value, and half of the smallest
+    subnormal.
+"""
+import numpy as np
+import pytest
+import torch
+
+import residual_binary_weight_b200 as rb
+from oracle import block8
+from gpu_util import rows_to_sliced
+
+pytestmark = pytest.mark.gpu
+
+NAMES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+U = 2.0 ** -24
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def out_round(y, dt):
+    i = torch.finfo(dt)
+    return np.abs(y) * (i.eps / 2) + i.smallest_normal * i.eps / 2
+
+
+def mags(x, name):
+    """Magnitudes as they count in D."""
+    return np.maximum(np.abs(x), torch.finfo(NAMES[name]).smallest_normal)
+
+
+def close(got, ref, tol, dt):
+    got = f64(got)
+    assert got.shape == ref.shape
+    lim = tol + out_round(np.abs(ref) + tol, dt)
+    err = np.abs(got - ref)
+    assert np.isfinite(got).all()
+    assert (err <= lim).all(), float((err / np.maximum(lim, 1e-300)).max())
+
+
+def padded(x, pad, fill=float("nan")):
+    """x in a buffer whose rows are `pad` values longer."""
+    big = torch.full((x.shape[0], x.shape[1] + pad), fill, dtype=x.dtype, device="cuda")
+    big[:, :x.shape[1]] = x
+    return big[:, :x.shape[1]]
+
+
+def values(rng, rows, K, name):
+    x = rng.standard_normal((rows, K)) * np.exp(1.5 * rng.standard_normal((rows, 1)))
+    x[:, rng.integers(0, K, max(1, K // 100))] *= 30
+    return torch.from_numpy(x.astype(np.float32)).to(NAMES[name]).cuda()
+
+
+def codes_of(rng, rows, K, block_rows, any_scale=False):
+    """Random codes (no NaN) and scales: powers of two, or any."""
+    c = rng.integers(0, 127, (rows, K)).astype(np.uint8) | (rng.integers(0, 2, (rows, K)) << 7).astype(np.uint8)
+    n = rng.integers(-12, 3, (-(-rows // block_rows), K // 128))
+    s = np.ldexp(1.0, n)
+    if any_scale:
+        s = (s * rng.uniform(1, 2, s.shape)).astype(np.float32).astype(np.float64)
+    return c, s
+
+
+def dev_codes(c, s):
+    return torch.from_numpy(c).view(torch.float8_e4m3fn).cuda(), torch.from_numpy(s.astype(np.float32)).cuda()
+
+
+# ---------------------------------------------------------------- pack, unpack
+def check_pack(x, block_rows, name):
+    c, s = rb.pack8(x, block_rows=block_rows)
+    torch.cuda.synchronize()
+    rc, rs = block8.pack8(f64(x), block_rows, name)
+    assert np.array_equal(f64(s), rs)
+    got = c.view(torch.uint8).cpu().numpy()
+    zero = (got & 0x7F) == 0                     # -0 and +0 stand for the same value
+    assert np.array_equal(np.where(zero, 0, got), np.where((rc & 0x7F) == 0, 0, rc))
+    return c, s
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("rows,K,pad", [(1, 128, 0), (3, 384, 8), (127, 128, 0), (129, 256, 24), (300, 1152, 0)])
+def test_pack8_matches_oracle(name, block_rows, rows, K, pad):
+    rng = np.random.default_rng(rows + K + block_rows)
+    x = values(rng, rows, K, name)
+    x[0, :128] = 0
+    check_pack(padded(x, pad) if pad else x, block_rows, name)
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_pack8_edges(name, block_rows):
+    """Scale borders, ties, subnormals, the largest values, infinities and NaN."""
+    dt = NAMES[name]
+    i = torch.finfo(dt)
+    x = torch.zeros((11, 256), dtype=torch.float64)
+    x[0, 3] = 448.0                                         # exactly 448 * 2^0
+    x[1, 3] = 448.0 * (1 + i.eps)                           # the next value: scale 2
+    x[2, 7] = i.max
+    x[2, 8:12] = torch.tensor([-i.max, i.max * 0.93, 1.0, 100.0])
+    x[3, 1] = i.smallest_normal * i.eps                     # smallest subnormal
+    x[4, :4] = torch.tensor([float("inf"), 1.0, -3.0, 0.5])
+    x[4, 130] = float("nan")
+    x[5, :] = float("nan")
+    x[6, :] = -float("inf")
+    x[7, :17] = 1.0 + torch.arange(17, dtype=torch.float64) / 16      # ties between e4m3 values
+    x[8, :9] = 448.0
+    x[8, 1:9] = torch.arange(8, dtype=torch.float64) * 2.0 ** -10     # e4m3 subnormals and their ties
+    x[9, 128:] = -0.0
+    x[10, :] = 447.9
+    check_pack(x.to(dt).cuda(), block_rows, name)
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("block_rows,rows,K,pad", [(1, 1, 128, 0), (1, 77, 640, 8), (128, 130, 256, 16), (128, 5, 4096, 0)])
+def test_unpack8_is_the_rounded_product(name, block_rows, rows, K, pad):
+    rng = np.random.default_rng(rows * K)
+    c, s = codes_of(rng, rows, K, block_rows, any_scale=True)
+    big = torch.full((rows, K + pad), 7.0, dtype=NAMES[name], device="cuda")
+    got = rb.unpack8(*dev_codes(c, s), block_rows=block_rows, X=big[:, :K])
+    # code * scale in fp32 (4 + 24 bits: one rounding), then to the type
+    ref = torch.from_numpy(block8.unpack8(c, s, block_rows)).float().to(NAMES[name])
+    assert torch.equal(got.cpu(), ref)
+    assert (big[:, K:] == 7.0).all(), "wrote past the row"
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16", "f32"])
+def test_unpack8_of_pack8_is_within_half_a_step(name):
+    rng = np.random.default_rng(4)
+    x = values(rng, 50, 512, name)
+    c, s = rb.pack8(x)
+    y = rb.unpack8(c, s, dtype=NAMES[name])
+    assert np.array_equal(f64(y), block8.unpack8(c.view(torch.uint8).cpu().numpy(), f64(s), 1))    # exact in the type
+    step = np.maximum(2.0 ** -4 * np.abs(f64(x)), 2.0 ** -10 * np.repeat(f64(s), 128, 1))
+    assert (np.abs(f64(y) - f64(x)) <= step).all()
+
+
+# ----------------------------------------------------------------------- gemm8
+def gemm8_tol(D, G):
+    return (2.0 ** -16 + (G + 10) * U) * D
+
+
+def check_gemm8(rng, T, M, K, name="f16", pad=0, any_scale=False):
+    w, ws = codes_of(rng, M, K, 128, any_scale)
+    x, xs = codes_of(rng, T, K, 1, any_scale)
+    ws, xs = ws * 2.0 ** -6, xs * 2.0 ** -6
+    big = torch.full((T, M + pad), float("nan"), dtype=NAMES[name], device="cuda")
+    y = rb.gemm8(*dev_codes(w, ws), *dev_codes(x, xs), Y=big[:, :M], check_device=True)
+    ref, D = block8.gemm8(w, ws, x, xs)
+    close(y, ref, gemm8_tol(D, K // 128), NAMES[name])
+    assert torch.isnan(big[:, M:]).all(), "wrote past the row"
+
+
+@pytest.mark.parametrize("T", [1, 2, 9, 16, 33, 100, 128, 129, 300])
+@pytest.mark.parametrize("M,K", [(1, 128), (100, 640), (256, 1024), (515, 2176)])
+def test_gemm8_matches_oracle(T, M, K):
+    check_gemm8(np.random.default_rng(T + M + K), T, M, K)
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("pad", [0, 1, 8])
+def test_gemm8_types_pitches_and_any_scales(name, pad):
+    check_gemm8(np.random.default_rng(pad), 37, 331, 512, name, pad, any_scale=True)
+
+
+@pytest.mark.parametrize("T,M,K,name", [(1280, 4001, 256, "f16"), (2500, 2048, 384, "bf16"), (70, 40000, 128, "f32")])
+def test_gemm8_many_tiles(T, M, K, name):
+    check_gemm8(np.random.default_rng(T), T, M, K, name)
+
+
+def test_gemm8_nan_codes_stay_in_their_row_and_column():
+    rng = np.random.default_rng(8)
+    w, ws = codes_of(rng, 140, 256, 128)
+    x, xs = codes_of(rng, 20, 256, 1)
+    w[133, 200], x[3, 5] = 0x7F, 0xFF
+    y = f64(rb.gemm8(*dev_codes(w, ws * 2.0 ** -6), *dev_codes(x, xs * 2.0 ** -6), y_dtype=torch.float32))
+    bad = np.isnan(y)
+    assert bad[3].all() and bad[:, 133].all()
+    bad[3], bad[:, 133] = False, False
+    assert not bad.any()
+
+
+# ----------------------------------------------------------------------- wgrad
+def gradient(rng, T, M, dt, pad=0):
+    g = torch.from_numpy((rng.standard_normal((T, M)) * 0.1).astype(np.float32)).to(dt).cuda()
+    return padded(g, -M % 8 + pad) if (M % 8 or pad) else g
+
+
+def check_wgrad(rng, T, M, K, name="f16", out="f32", add=None, any_scale=False, pad=0):
+    c, s = codes_of(rng, T, K, 1, any_scale)
+    s = s * 2.0 ** -4
+    dy = gradient(rng, T, M, NAMES[name], pad)
+    base = None
+    if add:
+        base = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).to(NAMES[out]).cuda()
+    want_base = 0.0 if base is None else f64(base)
+    dw = rb.gemm_wgrad(dy, *dev_codes(c, s), add=base, dW=base if add == "in place" else None, dw_dtype=NAMES[out],
+                       check_device=True)
+    # the operand is code * scale rounded to dY's type (also where the scale is
+    # a power of two: a code of 2^-9 with a scale of 2^-16 is below fp16's 2^-24)
+    x = torch.from_numpy(block8.unpack8(c, s, 1)).float().to(NAMES[name]).double().numpy()
+    ref, D = block8.wgrad(f64(dy), x)[0], mags(f64(dy), name).T @ mags(x, name)
+    close(dw, ref + want_base, (T + 1) * 2.0 ** -23 * (D + np.abs(want_base)), NAMES[out])
+    return dw, base
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("T", [1, 2, 63, 64, 65, 333])
+@pytest.mark.parametrize("M,K", [(1, 128), (64, 128), (100, 384), (257, 256), (640, 1152)])
+def test_wgrad_matches_oracle(name, T, M, K):
+    check_wgrad(np.random.default_rng(T + M + K), T, M, K, name)
+
+
+@pytest.mark.parametrize("name,out", [("f16", "f16"), ("bf16", "bf16"), ("f16", "bf16"), ("bf16", "f16"), ("bf16", "f32")])
+@pytest.mark.parametrize("add", [None, "apart", "in place"])
+def test_wgrad_output_types_and_sums(name, out, add):
+    dw, base = check_wgrad(np.random.default_rng(6), 130, 264, 256, name, out, add)
+    assert (dw is base) == (add == "in place")
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+def test_wgrad_any_scale_and_pitches(name):
+    check_wgrad(np.random.default_rng(7), 90, 200, 384, name, any_scale=True, pad=16)
+
+
+def test_wgrad_many_tiles():
+    check_wgrad(np.random.default_rng(11), 200, 2600, 2048, "bf16", "bf16", "apart")
+
+
+def test_wgrad_long_sequence_few_tiles():
+    check_wgrad(np.random.default_rng(12), 20000, 72, 128, "f16")
+
+
+def test_wgrad_writes_only_its_columns():
+    rng = np.random.default_rng(13)
+    c, s = codes_of(rng, 40, 128, 1)
+    big = torch.full((70, 200), float("nan"), device="cuda")
+    rb.gemm_wgrad(gradient(rng, 40, 70, torch.float16), *dev_codes(c, s), dW=big[:, :128])
+    assert torch.isnan(big[:, 128:]).all() and torch.isfinite(big[:, :128]).all()
+
+
+def test_wgrad_non_finite_values_reach_their_row_and_column_only():
+    rng = np.random.default_rng(14)
+    c, s = codes_of(rng, 70, 256, 1)
+    dy = gradient(rng, 70, 90, torch.float16)
+    c[69, 17] = 0x7F
+    dy[3, 5] = float("inf")
+    dw = f64(rb.gemm_wgrad(dy, *dev_codes(c, s)))
+    bad = ~np.isfinite(dw)
+    assert bad[5].all() and np.isnan(dw[:, 17]).all()
+    bad[5], bad[:, 17] = False, False
+    assert not bad.any()
+
+
+# ----------------------------------------------------------------------- dgrad
+def plane_case(rng, M, K, N, group, f16):
+    planes = rng.integers(0, 2 ** 32, (N, M, K // 32), dtype=np.uint64).astype(np.uint32)
+    a = 0.5 ** np.arange(N)[:, None, None] * rng.uniform(0.5, 1.5, (N, M, K // 128 if group else 1))
+    a = a.astype(np.float16 if f16 else np.float32)
+    return planes, a
+
+
+def check_dgrad(rng, T, M, K, N=2, group=0, f16=False, order="rows", name="f16", out=None, pad=0, opad=0):
+    planes, a = plane_case(rng, M, K, N, group, f16)
+    dy = gradient(rng, T, M, NAMES[name], pad)
+    out = NAMES[out or name]
+    p = rows_to_sliced(planes) if order == "sliced" else planes
+    big = torch.full((T, K + opad), float("nan"), dtype=out, device="cuda")
+    dx = rb.gemm_dgrad(torch.from_numpy(p.view(np.int32)).cuda(), torch.from_numpy(a).cuda(), dy, K, group=group,
+                       dX=big[:, :K], check_device=True)
+    ref, D = block8.dgrad(f64(dy), planes, a.astype(np.float64))
+    # D is over |W^|, the scales' fp32 sum is rounded relative to sum |alpha|
+    Da = np.abs(f64(dy)) @ np.repeat(np.abs(a.astype(np.float64)).sum(0), K // a.shape[2], 1)
+    eps = torch.finfo(NAMES[name]).eps
+    tiny = torch.finfo(NAMES[name]).smallest_normal * eps / 2        # the operand's subnormal step
+    Dm = mags(f64(dy), name) @ mags(block8.weight(planes, a), name)
+    tol = eps / 2 * D + M * 2.0 ** -23 * Dm + 3 * U * Da + tiny * np.abs(f64(dy)).sum(1, keepdims=True)
+    close(dx, ref, tol, out)
+    assert torch.isnan(big[:, K:]).all(), "wrote past the row"
+
+
+@pytest.mark.parametrize("N,group,f16", [(1, 0, False), (2, 0, False), (2, 0, True), (3, 0, False), (4, 0, True),
+                                         (1, 128, True), (2, 128, False), (4, 128, True)])
+@pytest.mark.parametrize("order", ["rows", "sliced"])
+@pytest.mark.parametrize("T,M,K,name", [(1, 64, 128, "f16"), (5, 200, 640, "bf16"), (70, 333, 256, "f16")])
+def test_dgrad_layouts(N, group, f16, order, T, M, K, name):
+    check_dgrad(np.random.default_rng(T + N + group), T, M, K, N, group, f16, order, name)
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("T", [1, 31, 32, 33, 64, 65, 128, 129, 256, 257, 600])
+@pytest.mark.parametrize("M,K", [(1, 128), (65, 384), (515, 1024)])
+def test_dgrad_matches_oracle(name, T, M, K):
+    check_dgrad(np.random.default_rng(T + M), T, M, K, name=name)
+
+
+@pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("pad,opad", [(0, 0), (8, 3)])
+def test_dgrad_output_types_and_pitches(out, pad, opad):
+    check_dgrad(np.random.default_rng(2), 45, 130, 256, name="bf16", out=out, pad=pad, opad=opad)
+
+
+def test_dgrad_many_tiles():
+    check_dgrad(np.random.default_rng(15), 1500, 300, 4096, order="sliced", name="bf16")
+
+
+def test_dgrad_agrees_with_differences_of_the_forward():
+    """<C, gemm(x + e) - gemm(x - e)> / 2 against <dX, e>: the forward is linear
+    in x (planes fixed), so the difference is the derivative but for both
+    kernels' roundings, which their own bounds cover."""
+    rng = np.random.default_rng(16)
+    T, M, K = 20, 96, 256
+    planes, a = plane_case(rng, M, K, 2, 0, False)
+    p, al = torch.from_numpy(planes.view(np.int32)).cuda(), torch.from_numpy(a).cuda()
+    C = gradient(rng, T, M, torch.float16)
+    dx, D = f64(rb.gemm_dgrad(p, al, C, K, dx_dtype=torch.float32)), block8.dgrad(f64(C), planes, a)[1]
+    W = np.abs(block8.weight(planes, a))
+    x = torch.from_numpy(rng.integers(-8, 9, (T, K)).astype(np.float16)).cuda()
+    for t, j in [(0, 0), (3, 77), (19, 255)]:
+        e = torch.zeros_like(x)
+        e[t, j] = 2.0
+        up, dn = f64(rb.gemm(p, al, x + e, y_dtype=torch.float32)), f64(rb.gemm(p, al, x - e, y_dtype=torch.float32))
+        diff = (f64(C) * (up - dn)).sum() / 4
+        # each forward output carries fp32 sums of 2 K products: 2 K 2^-23 of its scale
+        fwd = 2 * K * 2.0 ** -23 * (np.abs(f64(x)) + 2) @ (W.max() * np.ones((K, M)))
+        Dm = mags(f64(C), "f16") @ mags(block8.weight(planes, a), "f16")
+        tol = (2.0 ** -11 + 3 * U) * D[t, j] + M * 2.0 ** -23 * Dm[t, j] + (np.abs(f64(C)) * fwd).sum() / 2
+        assert abs(diff - dx[t, j]) <= tol
+
+
+# ------------------------------------------------------- as they are used together
+def test_training_step_of_a_layer():
+    """Forward from W with its input kept in 8 bits, then both gradients, the
+    weight's summed over two micro-batches, and a step of the weight."""
+    rng = np.random.default_rng(17)
+    T, M, K = 96, 192, 256
+    W = torch.from_numpy((rng.standard_normal((M, K)) * 0.05).astype(np.float16)).cuda()
+    grad = torch.zeros((M, K), device="cuda")
+    want = np.zeros((M, K))
+    tol = np.zeros((M, K))
+    planes, alpha, _ = rb.pack(W, 2, order="sliced")
+    for _ in range(2):
+        X = values(rng, T, K, "f16")
+        Y = rb.gemm_from_weight(W, X, n_paths=2)
+        assert torch.equal(Y, rb.gemm(planes, alpha, X))
+        codes, scales = rb.pack8(X)
+        dY = gradient(rng, T, M, torch.float16)
+        dX = rb.gemm_dgrad(planes, alpha, dY, K, check_device=True)
+        rows = planes.cpu().numpy().view(np.uint32)
+        rows = np.concatenate(list(rows.swapaxes(0, 1)), axis=2)[:, :, :K // 32]
+        ref, D = block8.dgrad(f64(dY), rows, f64(alpha))
+        Da = np.abs(f64(dY)) @ np.repeat(f64(alpha).sum(0), K, 1)
+        Dm = mags(f64(dY), "f16") @ mags(block8.weight(rows, f64(alpha)), "f16")
+        close(dX, ref, 2.0 ** -11 * D + M * 2.0 ** -23 * Dm + 3 * U * Da + 2.0 ** -25 * np.abs(f64(dY)).sum(1, keepdims=True),
+              torch.float16)
+        out = rb.gemm_wgrad(dY, codes, scales, add=grad, dW=grad, check_device=True)
+        assert out is grad
+        # against the gradient of the unrounded input: half an e4m3 step of each X
+        exact, _ = block8.wgrad(f64(dY), f64(X))
+        step = np.maximum(2.0 ** -4 * np.abs(f64(X)), 2.0 ** -10 * np.repeat(f64(scales), 128, 1))
+        want += exact
+        # fp32 sums, of |X| up to twice over (code * scale is within 2^-4 of X, or within the step)
+        tol += np.abs(f64(dY)).T @ step + (T + 1) * 2.0 ** -22 * (mags(f64(dY), "f16").T @ mags(f64(X), "f16") + np.abs(want))
+    close(grad, want, tol, torch.float32)
+
+
+def test_eight_bit_layer_next_to_its_checkpoint():
+    """The codes that feed gemm8 in the forward pass are the checkpoint of its weight gradient."""
+    rng = np.random.default_rng(18)
+    W, X = values(rng, 200, 384, "f32") * 0.01, values(rng, 40, 384, "bf16")
+    w, ws = rb.pack8(W, block_rows=128)
+    x, xs = rb.pack8(X)
+    y = rb.gemm8(w, ws, x, xs, y_dtype=torch.bfloat16, check_device=True)
+    wh, wsh, xh, xsh = (t.view(torch.uint8).cpu().numpy() if t.dtype == torch.float8_e4m3fn else f64(t) for t in (w, ws, x, xs))
+    ref, D = block8.gemm8(wh, wsh, xh, xsh)
+    close(y, ref, gemm8_tol(D, 3), torch.bfloat16)
+    dw = rb.gemm_wgrad(y, x, xs, check_device=True)
+    ref, D = block8.wgrad(f64(y), block8.unpack8(xh, xsh, 1))
+    close(dw, ref, 41 * 2.0 ** -23 * D, torch.float32)
+
+
+def _step(W, ws, X, dY, planes, alpha, bufs):
+    c, s = rb.pack8(X, codes=bufs["c"], scales=bufs["s"])
+    rb.unpack8(c, s, X=bufs["X"])
+    rb.gemm8(W, ws, c, s, Y=bufs["Y"], workspace=bufs["k0"])
+    rb.gemm_wgrad(dY, c, s, dW=bufs["dW"], workspace=bufs["k1"])
+    rb.gemm_dgrad(planes, alpha, dY, X.shape[1], dX=bufs["dX"], workspace=bufs["k2"])
+
+
+def _step_case(seed, T=70, M=300, K=512):
+    rng = np.random.default_rng(seed)
+    X = values(rng, T, K, "f16")
+    W, ws = rb.pack8(values(rng, M, K, "f32"), block_rows=128)
+    dY = gradient(rng, T, M, torch.float16)
+    planes, a = plane_case(rng, M, K, 2, 0, False)
+    bufs = {"c": torch.empty((T, K), dtype=torch.float8_e4m3fn, device="cuda"), "s": torch.empty((T, K // 128), device="cuda"),
+            "X": torch.empty((T, K), dtype=torch.float16, device="cuda"), "Y": torch.empty((T, M), dtype=torch.float16, device="cuda"),
+            "dW": torch.empty((M, K), device="cuda"), "dX": torch.empty((T, K), dtype=torch.float16, device="cuda"),
+            **{k: torch.empty(256, dtype=torch.uint8, device="cuda") for k in ("k0", "k1", "k2")}}
+    return W, ws, X, dY, torch.from_numpy(planes.view(np.int32)).cuda(), torch.from_numpy(a).cuda(), bufs
+
+
+def _bits(b):
+    return {k: b[k].view(torch.uint8).clone() for k in ("c", "s", "X", "Y", "dW", "dX")}
+
+
+def test_repeated_calls_give_the_same_bits():
+    case = _step_case(21)
+    _step(*case)
+    first = _bits(case[-1])
+    for _ in range(3):
+        _step(*case)
+    again = _bits(case[-1])
+    assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_captured_and_replayed_on_new_inputs():
+    case = _step_case(22)
+    X, dY, bufs = case[2], case[3], case[-1]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(*case)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _step(*case)
+    for seed in (23, 24):
+        rng = np.random.default_rng(seed)
+        X.copy_(values(rng, *X.shape, "f16"))
+        dY.copy_(gradient(rng, *dY.shape, torch.float16))
+        _step(*case)
+        want = _bits(bufs)
+        for k in ("c", "s", "X", "Y", "dW", "dX"):
+            bufs[k].view(torch.uint8).zero_()
+        g.replay()
+        got = _bits(bufs)
+        assert all(torch.equal(want[k], got[k]) for k in want)
+
+
+def test_two_streams_at_once():
+    cases = [_step_case(25), _step_case(26)]
+    want = []
+    for c in cases:
+        _step(*c)
+        want.append(_bits(c[-1]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(10):
+        for c, s in zip(cases, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                _step(*c)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        got = _bits(c[-1])
+        assert all(torch.equal(w[k], got[k]) for k in w)
+
+
+def test_check_reports_a_flag_and_the_next_call_clears_it():
+    W, ws, X, dY, planes, alpha, bufs = case = _step_case(27)
+    _step(*case)
+    calls = {"k0": lambda: rb.gemm8(W, ws, bufs["c"], bufs["s"], workspace=bufs["k0"], check_device=True),
+             "k1": lambda: rb.gemm_wgrad(dY, bufs["c"], bufs["s"], workspace=bufs["k1"], check_device=True),
+             "k2": lambda: rb.gemm_dgrad(planes, alpha, dY, X.shape[1], workspace=bufs["k2"], check_device=True)}
+    lib = rb.load()
+    for k, call in calls.items():
+        bufs[k].view(torch.int32)[1] = 2                  # what a kernel's atomicOr would leave
+        assert lib.rb_gemm_check(bufs[k].data_ptr(), torch.cuda.current_stream().cuda_stream) == 6
+        call()
+
+
+def test_binding_refusals():
+    W, ws, X, dY, planes, alpha, bufs = _step_case(28)
+    c, s = rb.pack8(X)
+    bad = [lambda: rb.pack8(X.t()), lambda: rb.pack8(X.int()), lambda: rb.pack8(X, block_rows=2),
+           lambda: rb.pack8(X, codes=c[:1]), lambda: rb.pack8(X, scales=s.t()), lambda: rb.pack8(X[0]),
+           lambda: rb.unpack8(c.view(torch.uint8), s), lambda: rb.unpack8(c, s[:, :1]), lambda: rb.unpack8(c, s, X=X[:5]),
+           lambda: rb.unpack8(c, s, dtype=torch.float64), lambda: rb.unpack8(c[:, ::2], s),
+           lambda: rb.gemm8(W, ws, c[:, :256].contiguous(), s[:, :2].contiguous()), lambda: rb.gemm8(W, s, c, s),
+           lambda: rb.gemm8(W, ws, c, s, Y=X), lambda: rb.gemm_wgrad(dY[:3], c, s), lambda: rb.gemm_wgrad(dY.float(), c, s),
+           lambda: rb.gemm_wgrad(dY, c, s, add=torch.zeros((300, 512), device="cuda"), dW=torch.zeros((300, 512), device="cuda").half()),
+           lambda: rb.gemm_wgrad(dY, c, s, add=torch.zeros((300, 640), device="cuda")[:, :512]),
+           lambda: rb.gemm_wgrad(dY, c, s, dw_dtype=torch.int32), lambda: rb.gemm_dgrad(planes, alpha, dY[:, :200], 512),
+           lambda: rb.gemm_dgrad(planes, alpha, dY, 256), lambda: rb.gemm_dgrad(planes, alpha[:1], dY, 512),
+           lambda: rb.gemm_dgrad(planes, alpha, dY, 512, group=128), lambda: rb.gemm_dgrad(planes, alpha, dY.float(), 512)]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            print("case", i, "was taken")
+    with pytest.raises(rb.RbError, match="multiple of 128"):
+        rb.pack8(X[:, :200].contiguous())
+    with pytest.raises(rb.RbError, match="ALIGNMENT"):
+        rb.gemm_wgrad(dY.contiguous()[:, :297].contiguous(), c, s)        # 594-byte rows
+    with pytest.raises(rb.RbError, match="positive"):
+        rb.pack8(X[:0])
