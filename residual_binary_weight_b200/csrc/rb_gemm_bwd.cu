@@ -13,7 +13,13 @@
 // K-major for dgrad (a row of dY runs along r = i), N-major for wgrad (it
 // runs along n = m).
 //
-// Roles (448 threads): warps 0-3 epilogue, 4-11 expansion, 12 TMA, 13 MMAs.
+// Three rings, each with its own full and empty barriers: C, the compressed
+// operand as it lies in HBM (TMA; 64 rows of 128 codes, or of 4 plane words
+// per path); A, its expansion; B, the dY tiles. The expansion only waits for
+// C and for a free slot of A, so neither load's latency meets it.
+//
+// Roles (480 threads): warps 0-3 epilogue, 4-11 expansion in two groups that
+// take the stages in turn, 12 B loads, 13 MMAs, 14 C loads.
 // A CTA walks its tiles with two accumulators, so the epilogue of a tile
 // overlaps the next tile's MMAs. Few tiles: a cluster of CTAs shares a
 // tile, each takes part of the rows r, and the sums meet in distributed
@@ -34,13 +40,29 @@ namespace {
 
 using namespace tc;
 
-constexpr int EPI_WARPS = 4, EXP_WARP0 = 4, EXP_WARPS = 8, TMA_WARP = 12, MMA_WARP = 13;
-constexpr int THREADS = 448;
+constexpr int EPI_WARPS = 4, EXP_WARP0 = 4, GROUP_WARPS = 4, GROUPS = 2;
+constexpr int B_WARP = 12, MMA_WARP = 13, C_WARP = 14;
+constexpr int THREADS = 480;
 constexpr int BR = 64;                          // rows r per stage
 constexpr uint32_t A_BYTES = 128 * BR * 2;      // two chunks of [64 r][64 j]
 constexpr uint32_t CHUNK = 64 * BR * 2;         // 8 KB
-constexpr int MAX_STAGES = 8;
 enum : int { DGRAD = 0, WGRAD = 1 };
+
+template <int MODE, int NP, int BN>
+struct BwCfg {
+    static constexpr uint32_t B_BYTES = BN * BR * 2;
+    static constexpr uint32_t C_BYTES = MODE == WGRAD ? 128 * BR : NP * 16 * BR;
+    static constexpr int AS = 3, BS = BN >= 256 ? 4 : 6, CS = MODE == WGRAD ? 5 : 6;
+    static constexpr uint32_t TILES = AS * A_BYTES + BS * B_BYTES + CS * C_BYTES;
+    static constexpr int BARS = 2 * (AS + BS + CS) + 4;
+    // at least 120 KB, so that two CTAs never share an SM's tensor memory
+    static constexpr uint32_t SMEM = (TILES < 119u * 1024u ? 119u * 1024u : TILES) + 1024u;
+    static constexpr uint32_t TMEM_COLS = 2 * BN;
+    static_assert(SMEM + 512 <= 227 * 1024, "shared memory");
+    static_assert(BN * 512u <= TILES || BN <= 128, "a split tile's sums do not fit the rings");
+    // the groups wait on slots that their own previous stage has passed
+    static_assert(GROUPS <= AS && GROUPS <= CS, "a group could run two phases ahead of a slot");
+};
 
 struct BwArgs {
     uint32_t* err;
@@ -52,7 +74,6 @@ struct BwArgs {
     void* out;
     int64_t R, N, J, ldo;       // contraction, output rows, output columns (K)
     int j_tiles, n_tiles;
-    int stages;
     int out_dt;
     bool sliced, alpha_f16, g128;
 };
@@ -114,107 +135,116 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
-// What one expansion thread holds of one stage: row r, 32 columns.
+// The scales of one row r of the compressed operand (0 past the last row, so
+// that the row adds nothing), read ahead of the row's stage.
 template <int MODE, int NP>
-struct Unit;
-
-template <int NP>
-struct Unit<DGRAD, NP> {
-    uint32_t w[NP];
-    float al[NP];
+struct Scales {
+    float v[NP];
     __device__ __forceinline__ void load(const BwArgs& a, int64_t r, int64_t j) {
-        const int64_t i = r < a.R ? r : a.R - 1;
-        const int64_t W32 = a.J >> 5, S = (a.J + 511) >> 9, gpr = a.J >> 7, word = j >> 5;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            w[p] = __ldg(a.sliced ? a.planes + ((p * S + (word >> 4)) * a.R + i) * 16 + (word & 15)
-                                  : a.planes + (p * a.R + i) * W32 + word);
-            const int64_t ai = a.g128 ? (p * a.R + i) * gpr + (j >> 7) : p * a.R + i;
-            const float v = a.alpha_f16 ? __half2float(__ldg(static_cast<const __half*>(a.alpha) + ai))
-                                        : __ldg(static_cast<const float*>(a.alpha) + ai);
-            al[p] = r < a.R ? v : 0.0f;      // rows past the last: zeros
-        }
-    }
-    // the 32 weights sum_p +-alpha_p: path 0 gives the sign, the paths that
-    // agree or disagree with it choose one of 2^(NP-1) magnitudes
-    template <bool BF16>
-    __device__ __forceinline__ void expand(uint32_t (&h)[16]) const {
-        constexpr int NM = 1 << (NP - 1);
-        uint32_t mag[NM];
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            float v = al[0];
-#pragma unroll
-            for (int p = 1; p < NP; ++p) v += (m >> (p - 1)) & 1 ? al[p] : -al[p];
-            mag[m] = pack2<BF16>(v, v);
-        }
-        uint32_t s[NP][8];
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const uint32_t x = p == 0 ? w[0] : ~(w[0] ^ w[p]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) s[p][k] = x << (7 - k);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            // columns 2i and 2i+1: bit 8b + 2m (+ 1) is the top bit of byte b of s[2m (+ 1)]
-            const int m = i & 3, b = i >> 2;
-            const uint32_t lo = 8u | b, hi = 8u | (4u + b);
-            uint32_t v[NM];
-#pragma unroll
-            for (int k = 0; k < NM; ++k) v[k] = mag[k];
-#pragma unroll
-            for (int p = 1; p < NP; ++p) {
-                const uint32_t mask = prmt(s[p][2 * m], s[p][2 * m + 1], lo | (lo << 4) | (hi << 8) | (hi << 12));
-#pragma unroll
-                for (int k = 0; k < (NM >> p); ++k) v[k] = (mask & v[2 * k + 1]) | (~mask & v[2 * k]);
+            v[p] = 0.0f;
+            if (r < a.R) {
+                if constexpr (MODE == WGRAD) {
+                    v[p] = __ldg(a.scales + r * (a.J >> 7) + (j >> 7));
+                } else {
+                    const int64_t i = p * a.R + r, at = a.g128 ? i * (a.J >> 7) + (j >> 7) : i;
+                    v[p] = a.alpha_f16 ? __half2float(__ldg(static_cast<const __half*>(a.alpha) + at))
+                                       : __ldg(static_cast<const float*>(a.alpha) + at);
+                }
             }
-            const uint32_t sgn = prmt(s[0][2 * m], s[0][2 * m + 1], (lo << 4) | (hi << 12));
-            h[i] = v[0] ^ (~sgn & 0x80008000u);
         }
     }
 };
 
-template <int NP>
-struct Unit<WGRAD, NP> {
-    uint4 c0, c1;
-    float s;
-    __device__ __forceinline__ void load(const BwArgs& a, int64_t r, int64_t j) {
-        if (r < a.R) {
-            const uint4* p = reinterpret_cast<const uint4*>(a.codes + r * a.J + j);
-            c0 = __ldg(p);
-            c1 = __ldg(p + 1);
-            s = __ldg(a.scales + r * (a.J >> 7) + (j >> 7));
-        } else {
-            c0 = c1 = make_uint4(0u, 0u, 0u, 0u);
-            s = 0.0f;
+// 32 weights sum_p +-al_p from the 32 bits of w[p]: path 0 gives the sign, the
+// paths that agree or disagree with it choose one of 2^(NP-1) magnitudes.
+template <int NP, bool BF16>
+__device__ __forceinline__ void expand_planes(const uint32_t (&w)[NP], const float (&al)[NP], uint32_t (&h)[16]) {
+    constexpr int NM = 1 << (NP - 1);
+    uint32_t mag[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+        float v = al[0];
+#pragma unroll
+        for (int p = 1; p < NP; ++p) v += (m >> (p - 1)) & 1 ? al[p] : -al[p];
+        mag[m] = pack2<BF16>(v, v);
+    }
+    uint32_t s[NP][8];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const uint32_t x = p == 0 ? w[0] : ~(w[0] ^ w[p]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[p][k] = x << (7 - k);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        // columns 2i and 2i+1: bit 8b + 2m (+ 1) is the top bit of byte b of s[2m (+ 1)]
+        const int m = i & 3, b = i >> 2;
+        const uint32_t lo = 8u | b, hi = 8u | (4u + b);
+        uint32_t v[NM];
+#pragma unroll
+        for (int k = 0; k < NM; ++k) v[k] = mag[k];
+#pragma unroll
+        for (int p = 1; p < NP; ++p) {
+            const uint32_t mask = prmt(s[p][2 * m], s[p][2 * m + 1], lo | (lo << 4) | (hi << 8) | (hi << 12));
+#pragma unroll
+            for (int k = 0; k < (NM >> p); ++k) v[k] = (mask & v[2 * k + 1]) | (~mask & v[2 * k]);
+        }
+        const uint32_t sgn = prmt(s[0][2 * m], s[0][2 * m + 1], (lo << 4) | (hi << 12));
+        h[i] = v[0] ^ (~sgn & 0x80008000u);
+    }
+}
+
+// 32 codes times the row's scale
+template <bool BF16>
+__device__ __forceinline__ void expand_codes(const uint32_t (&c)[8], float s, uint32_t (&h)[16]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
+            : "=r"(h[2 * i]), "=r"(h[2 * i + 1])
+            : "r"(c[i]));
+    }
+    // a scale that fp16 holds exactly: one fp16 product rounds s c once
+    const __half sh = __float2half_rn(s);
+    if (!BF16 && __half2float(sh) == s) {
+        const __half2 s2 = __half2half2(sh);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), s2);
+            h[i] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+            h[i] = pack2<BF16>(f.x * s, f.y * s);
         }
     }
-    template <bool BF16>
-    __device__ __forceinline__ void expand(uint32_t (&h)[16]) const {
-        const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\t"
-                "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, u;\n\t}"
-                : "=r"(h[2 * i]), "=r"(h[2 * i + 1])
-                : "r"(c[i]));
-        }
-        // a scale that fp16 holds exactly: one fp16 product rounds s c once
-        const __half sh = __float2half_rn(s);
-        if (!BF16 && __half2float(sh) == s) {
-            const __half2 s2 = __half2half2(sh);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), s2);
-                h[i] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-                h[i] = pack2<BF16>(f.x * s, f.y * s);
-            }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// A ring position: slot and phase parity, advanced by one stage.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int by = 1) {
+        slot += by;
+        if (slot >= N) {
+            slot -= N;
+            ph ^= 1u;
         }
     }
 };
@@ -230,36 +260,73 @@ __device__ __forceinline__ void store_out(void* p, int dt, int64_t i, float v) {
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ void to_out(float v, float* p) { *p = v; }
+__device__ __forceinline__ void to_out(float v, __half* p) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void to_out(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
+
+// One column of up to 32 output rows (add + v), all loads before the first store.
+template <typename T>
+__device__ __forceinline__ void store_rows(void* out, const void* add, int64_t at, int64_t ldo, int left,
+                                           const uint32_t (&v)[32]) {
+    T* o = static_cast<T*>(out) + at;
+    const T* ad = static_cast<const T*>(add) + at;
+    T r[32];
+    if (left >= 32) {
+        if (add) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = ad[i * ldo];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) to_out(__uint_as_float(v[i]) + static_cast<float>(r[i]), o + i * ldo);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) to_out(__uint_as_float(v[i]), o + i * ldo);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left) to_out(__uint_as_float(v[i]) + (add ? static_cast<float>(ad[i * ldo]) : 0.0f), o + i * ldo);
+    }
+}
+
 template <int MODE, int NP, int BN, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
-gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, BwArgs a) {
-    constexpr uint32_t B_BYTES = BN * BR * 2, STAGE = A_BYTES + B_BYTES;
-    constexpr uint32_t TMEM_COLS = 2 * BN < 32 ? 32 : 2 * BN;
-    constexpr int PD = 3;                    // stages of compressed operand held in registers ahead of use
+gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap cmap, BwArgs a) {
+    using C = BwCfg<MODE, NP, BN>;
+    constexpr int AS = C::AS, BS = C::BS, CS = C::CS;
     extern __shared__ __align__(1024) unsigned char dsm[];
-    __shared__ __align__(8) uint64_t bars[3 * MAX_STAGES + 4];
+    __shared__ __align__(8) uint64_t bars[C::BARS];
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t abort_word;
     volatile uint32_t* abort_flag = &abort_word;
     const uint32_t tiles = (smem_addr(dsm) + 1023u) & ~1023u;
-    const int stages = a.stages;
-    auto a_tile = [&](int s) { return tiles + static_cast<uint32_t>(s) * STAGE; };
-    auto b_tile = [&](int s) { return tiles + static_cast<uint32_t>(s) * STAGE + A_BYTES; };
+    auto a_tile = [&](int s) { return tiles + static_cast<uint32_t>(s) * A_BYTES; };
+    auto b_tile = [&](int s) { return tiles + AS * A_BYTES + static_cast<uint32_t>(s) * C::B_BYTES; };
+    auto c_tile = [&](int s) { return tiles + AS * A_BYTES + BS * C::B_BYTES + static_cast<uint32_t>(s) * C::C_BYTES; };
     const uint32_t bar0 = smem_addr(bars);
-    auto full_b = [&](int s) { return bar0 + 8u * s; };
-    auto full_a = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + s); };
-    auto acc_full = [&](int b) { return bar0 + 8u * (3 * MAX_STAGES + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (3 * MAX_STAGES + 2 + b); };
+    auto full_a = [&](int s) { return bar0 + 8u * s; };
+    auto empty_a = [&](int s) { return bar0 + 8u * (AS + s); };
+    auto full_b = [&](int s) { return bar0 + 8u * (2 * AS + s); };
+    auto empty_b = [&](int s) { return bar0 + 8u * (2 * AS + BS + s); };
+    auto full_c = [&](int s) { return bar0 + 8u * (2 * AS + 2 * BS + s); };
+    auto empty_c = [&](int s) { return bar0 + 8u * (2 * AS + 2 * BS + CS + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (2 * (AS + BS + CS) + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * (AS + BS + CS) + 2 + b); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* err = a.err;
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;      // flags are raised only by waits that ran out
     if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) {
+        for (int s = 0; s < AS; ++s) {
+            mbar_init(full_a(s), GROUP_WARPS);
+            mbar_init(empty_a(s), 1);
+        }
+        for (int s = 0; s < BS; ++s) {
             mbar_init(full_b(s), 1);
-            mbar_init(full_a(s), EXP_WARPS);
-            mbar_init(empty_bar(s), 1);
+            mbar_init(empty_b(s), 1);
+        }
+        for (int s = 0; s < CS; ++s) {
+            mbar_init(full_c(s), 1);
+            mbar_init(empty_c(s), GROUP_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
@@ -268,7 +335,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, BwArgs a) {
         abort_word = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == MMA_WARP) tmem_alloc(smem_addr(&tmem_slot), TMEM_COLS);
+    if (warp == MMA_WARP) tmem_alloc(smem_addr(&tmem_slot), C::TMEM_COLS);
     fence_before();
     __syncthreads();
     fence_after();
@@ -281,45 +348,74 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, BwArgs a) {
     const int u0 = SPLIT ? blockIdx.x / size : blockIdx.x;
     const int u_step = SPLIT ? units : gridDim.x;
 
-    if (warp == TMA_WARP) {
+    if (warp == B_WARP) {
         if (lane == 0) {
+            Ring<BS> q;
             int it = 0;
             bool ok = true;
             for (int u = u0; u < units && ok; u += u_step) {
                 const int nt = u / a.j_tiles;
-                for (int rb = r_lo; rb < r_hi; ++rb, ++it) {
-                    const int s = it % stages;
-                    if (!mbar_wait(empty_bar(s), (static_cast<uint32_t>(it / stages) & 1u) ^ 1u, abort_flag, err, 1u)) {
+                for (int rb = r_lo; rb < r_hi; ++rb, ++it, q.next()) {
+                    if (!mbar_wait(empty_b(q.slot), q.ph ^ 1u, abort_flag, err, 1u)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(full_b(s), B_BYTES);
+                    mbar_arrive_expect_tx(full_b(q.slot), C::B_BYTES);
                     if constexpr (MODE == DGRAD) {
-                        tma_load_2d(b_tile(s), &dmap, rb * BR, nt * BN, full_b(s));
+                        tma_load_2d(b_tile(q.slot), &dmap, rb * BR, nt * BN, full_b(q.slot));
                     } else {
 #pragma unroll
                         for (int c = 0; c < BN / 64; ++c)
-                            tma_load_2d(b_tile(s) + c * CHUNK, &dmap, nt * BN + c * 64, rb * BR, full_b(s));
+                            tma_load_2d(b_tile(q.slot) + c * CHUNK, &dmap, nt * BN + c * 64, rb * BR, full_b(q.slot));
                     }
                 }
             }
             // after an abort the loads in flight land before the CTA gives up its shared memory
             if (*abort_flag)
-                for (int i = it - 1; i >= 0 && i >= it - stages; --i)
-                    mbar_drain(full_b(i % stages), static_cast<uint32_t>(i / stages) & 1u);
+                for (int i = it - 1; i >= 0 && i >= it - BS; --i)
+                    mbar_drain(full_b(i % BS), static_cast<uint32_t>(i / BS) & 1u);
+        }
+    } else if (warp == C_WARP) {
+        if (lane == 0) {
+            Ring<CS> q;
+            int it = 0;
+            bool ok = true;
+            const int S = static_cast<int>((a.J + 511) >> 9);
+            for (int u = u0; u < units && ok; u += u_step) {
+                const int jt = u % a.j_tiles;
+                for (int rb = r_lo; rb < r_hi; ++rb, ++it, q.next()) {
+                    if (!mbar_wait(empty_c(q.slot), q.ph ^ 1u, abort_flag, err, 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(full_c(q.slot), C::C_BYTES);
+                    if constexpr (MODE == WGRAD) {
+                        tma_load_3d(c_tile(q.slot), &cmap, jt * 128, rb * BR, 0, full_c(q.slot));
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) {
+                            const int x = a.sliced ? (jt & 3) * 4 : jt * 4, z = a.sliced ? p * S + (jt >> 2) : p;
+                            tma_load_3d(c_tile(q.slot) + p * 16 * BR, &cmap, x, rb * BR, z, full_c(q.slot));
+                        }
+                    }
+                }
+            }
+            if (*abort_flag)
+                for (int i = it - 1; i >= 0 && i >= it - CS; --i)
+                    mbar_drain(full_c(i % CS), static_cast<uint32_t>(i / CS) & 1u);
         }
     } else if (warp == MMA_WARP) {
         constexpr uint32_t idesc = idesc_bw(BN, BF16, MODE == WGRAD);
-        int it = 0, tile = 0;
+        Ring<AS> qa;
+        Ring<BS> qb;
+        int tile = 0;
         bool ok = true;
         for (int u = u0; u < units && ok; u += u_step, ++tile) {
             const int b = tile & 1;
             ok = __all_sync(FULL_MASK, mbar_wait(acc_empty(b), (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u, abort_flag, err, 2u));
-            for (int rb = r_lo; rb < r_hi && ok; ++rb, ++it) {
-                const int s = it % stages;
-                const uint32_t ph = static_cast<uint32_t>(it / stages) & 1u;
-                if (!__all_sync(FULL_MASK, mbar_wait(full_b(s), ph, abort_flag, err, 2u) &&
-                                               mbar_wait(full_a(s), ph, abort_flag, err, 2u))) {
+            for (int rb = r_lo; rb < r_hi && ok; ++rb, qa.next(), qb.next()) {
+                if (!__all_sync(FULL_MASK, mbar_wait(full_b(qb.slot), qb.ph, abort_flag, err, 2u) &&
+                                               mbar_wait(full_a(qa.slot), qa.ph, abort_flag, err, 2u))) {
                     ok = false;
                     break;
                 }
@@ -327,11 +423,13 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, BwArgs a) {
 #pragma unroll
                 for (int kk = 0; kk < BR / 16; ++kk) {
                     // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
-                    const uint64_t bd = MODE == DGRAD ? smem_desc(b_tile(s)) + 2u * kk : smem_desc_mn(b_tile(s) + 2048u * kk);
-                    umma_f16_elect(tmem + static_cast<uint32_t>(b * BN), smem_desc_mn(a_tile(s) + 2048u * kk), bd, idesc,
+                    const uint64_t bd = MODE == DGRAD ? smem_desc(b_tile(qb.slot)) + 2u * kk
+                                                      : smem_desc_mn(b_tile(qb.slot)) + 128u * kk;
+                    umma_f16_elect(tmem + static_cast<uint32_t>(b * BN), smem_desc_mn(a_tile(qa.slot)) + 128u * kk, bd, idesc,
                                    (rb > r_lo || kk > 0) ? 1u : 0u);
                 }
-                umma_commit_elect(empty_bar(s));
+                umma_commit_elect(empty_a(qa.slot));
+                umma_commit_elect(empty_b(qb.slot));
             }
             // also after an abort: the teardown waits for it
             umma_commit_elect(acc_full(b));
@@ -340,41 +438,70 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, BwArgs a) {
         if (!ok)
             for (int i = tile - 1; i >= 0 && i >= tile - 2; --i) mbar_drain(acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u);
     } else if (warp >= EXP_WARP0) {
-        const int e = warp - EXP_WARP0, wd = e & 3;
-        const int row = (e >> 2) * 32 + lane;                // row r within the stage
-        const uint32_t at = static_cast<uint32_t>(wd >> 1) * CHUNK + static_cast<uint32_t>(row) * 128u;
-        const uint32_t sw = static_cast<uint32_t>(row & 7), c0 = static_cast<uint32_t>(wd & 1) * 4u;
-        int it = 0;
+        const int grp = (warp - EXP_WARP0) / GROUP_WARPS, wd = (warp - EXP_WARP0) % GROUP_WARPS;
+        const uint32_t sw = static_cast<uint32_t>(lane & 7);
+        // this thread's rows of a stage are lane and lane + 32, its columns 32 wd .. 32 wd + 31
+        const uint32_t at = static_cast<uint32_t>(wd >> 1) * CHUNK + static_cast<uint32_t>(lane) * 128u;
+        const uint32_t c0 = static_cast<uint32_t>(wd & 1) * 4u;
+        Ring<AS> qa;
+        Ring<CS> qc;
         bool ok = true;
-        for (int u = u0; u < units && ok; u += u_step) {
+        int it = 0;                      // stages before this tile
+        qa.next(grp);
+        qc.next(grp);
+        for (int u = u0; u < units && ok; u += u_step, it += r_hi - r_lo) {
             const int64_t j = static_cast<int64_t>(u % a.j_tiles) * 128 + wd * 32;
-            Unit<MODE, NP> ring[PD];
+            int rb = r_lo + ((grp - it) & 1);          // the group's first stage of this tile
+            Scales<MODE, NP> cur[2], nxt[2];
 #pragma unroll
-            for (int i = 0; i < PD; ++i)
-                if (r_lo + i < r_hi) ring[i].load(a, static_cast<int64_t>(r_lo + i) * BR + row, j);
-            for (int rb0 = r_lo; rb0 < r_hi && ok; rb0 += PD) {
+            for (int k = 0; k < 2; ++k) {
+                cur[k].load(a, static_cast<int64_t>(rb) * BR + lane + 32 * k, j);
+                nxt[k].load(a, static_cast<int64_t>(rb + GROUPS) * BR + lane + 32 * k, j);
+            }
+            for (; rb < r_hi; rb += GROUPS, qa.next(GROUPS), qc.next(GROUPS)) {
+                Scales<MODE, NP> far[2];
 #pragma unroll
-                for (int i = 0; i < PD; ++i) {
-                    const int rb = rb0 + i;
-                    if (rb < r_hi && ok) {
-                        const int s = it % stages;
-                        uint32_t h[16];
-                        ring[i].template expand<BF16>(h);
-                        if (rb + PD < r_hi) ring[i].load(a, static_cast<int64_t>(rb + PD) * BR + row, j);
-                        if (!__all_sync(FULL_MASK, mbar_wait(empty_bar(s), (static_cast<uint32_t>(it / stages) & 1u) ^ 1u,
-                                                             abort_flag, err, 4u))) {
-                            ok = false;
-                        } else {
-                            const uint32_t base = a_tile(s) + at;
+                for (int k = 0; k < 2; ++k) far[k].load(a, static_cast<int64_t>(rb + 2 * GROUPS) * BR + lane + 32 * k, j);
+                if (!__all_sync(FULL_MASK, mbar_wait(full_c(qc.slot), qc.ph, abort_flag, err, 4u))) {
+                    ok = false;
+                    break;
+                }
+                uint32_t h[2][16];
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                sts128(base + (((c0 + c) ^ sw) << 4), h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
-                            fence_proxy_async_smem();   // make the generic-proxy stores visible to the tensor core
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(full_a(s));
-                            ++it;
-                        }
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t row = static_cast<uint32_t>(lane + 32 * k);
+                    if constexpr (MODE == WGRAD) {
+                        const uint32_t base = c_tile(qc.slot) + row * 128u;
+                        const uint4 x = lds128(base + (((2u * wd) ^ sw) << 4)), y = lds128(base + (((2u * wd + 1u) ^ sw) << 4));
+                        const uint32_t c[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                        expand_codes<BF16>(c, cur[k].v[0], h[k]);
+                    } else {
+                        uint32_t w[NP];
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) w[p] = lds32(c_tile(qc.slot) + p * 16u * BR + row * 16u + 4u * wd);
+                        expand_planes<NP, BF16>(w, cur[k].v, h[k]);
                     }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty_c(qc.slot));
+                if (!__all_sync(FULL_MASK, mbar_wait(empty_a(qa.slot), qa.ph ^ 1u, abort_flag, err, 4u))) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t base = a_tile(qa.slot) + at + static_cast<uint32_t>(k) * 4096u;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        sts128(base + (((c0 + c) ^ sw) << 4), h[k][4 * c], h[k][4 * c + 1], h[k][4 * c + 2], h[k][4 * c + 3]);
+                }
+                fence_proxy_async_smem();   // make the generic-proxy stores visible to the tensor core
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full_a(qa.slot));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    cur[k] = nxt[k];
+                    nxt[k] = far[k];
                 }
             }
         }
@@ -399,15 +526,11 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, BwArgs a) {
                     for (int i = 0; i < 32; ++i) buf[i * 128] = __uint_as_float(v[i]);
                 } else {
                     const int left = static_cast<int>(min(static_cast<int64_t>(32), a.N - n0 - c0));
-                    if (MODE == WGRAD && a.add) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < left)
-                                v[i] = __float_as_uint(__uint_as_float(v[i]) + load_out(a.add, a.out_dt, (n0 + c0 + i) * a.ldo + j));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < left) store_out(a.out, a.out_dt, (n0 + c0 + i) * a.ldo + j, __uint_as_float(v[i]));
+                    const int64_t at = (n0 + c0) * a.ldo + j;
+                    const void* add = MODE == WGRAD ? a.add : nullptr;
+                    if (a.out_dt == B8_F32) store_rows<float>(a.out, add, at, a.ldo, left, v);
+                    else if (a.out_dt == B8_F16) store_rows<__half>(a.out, add, at, a.ldo, left, v);
+                    else store_rows<__nv_bfloat16>(a.out, add, at, a.ldo, left, v);
                 }
             }
             fence_before();
@@ -437,15 +560,30 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, BwArgs a) {
         __syncthreads();
     }
     fence_after();
-    if (warp == MMA_WARP) tmem_dealloc(tmem, TMEM_COLS);
+    if (warp == MMA_WARP) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// Plane words in boxes of 4 words (one 128-column tile) x 64 rows of one path:
+// [N][M][K/32], or [N * S][M][16] in the sliced order.
+cudaError_t make_planes_map(CUtensorMap* map, const BwArgs& a, int n_paths) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t words = a.sliced ? 16 : static_cast<cuuint64_t>(a.J / 32);
+    const cuuint64_t dims[3] = {words, static_cast<cuuint64_t>(a.R),
+                                static_cast<cuuint64_t>(n_paths) * (a.sliced ? (a.J + 511) / 512 : 1)};
+    const cuuint64_t strides[2] = {words * 4, words * 4 * a.R};
+    const cuuint32_t box[3] = {4u, static_cast<cuuint32_t>(BR), 1u};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint32_t*>(a.planes), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
 }
 
 template <int MODE, int NP, int BN, bool BF16, bool SPLIT>
-cudaError_t launch(const CUtensorMap& m, BwArgs& a, int split, cudaStream_t s) {
-    constexpr size_t stage = A_BYTES + BN * BR * 2;
-    a.stages = static_cast<int>(std::min<size_t>(MAX_STAGES, (200 * 1024) / stage));
-    // at least 120 KB, so that two CTAs never share an SM's tensor memory
-    const size_t smem = std::max<size_t>(1024 + std::max<size_t>(a.stages * stage, SPLIT ? BN * 512 : 0), 120 * 1024);
+cudaError_t launch(const CUtensorMap& m, const CUtensorMap& c, BwArgs& a, int split, cudaStream_t s) {
+    constexpr size_t smem = BwCfg<MODE, NP, BN>::SMEM;
     auto kern = gemm_bwd_kernel<MODE, NP, BN, BF16, SPLIT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -461,31 +599,32 @@ cudaError_t launch(const CUtensorMap& m, BwArgs& a, int split, cudaStream_t s) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = SPLIT ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, m, a);
+    return cudaLaunchKernelEx(&cfg, kern, m, c, a);
 }
 
 template <int MODE, int NP, int BN>
-cudaError_t launch_bn(const CUtensorMap& m, BwArgs& a, bool bf16, cudaStream_t s) {
+cudaError_t launch_bn(const CUtensorMap& m, const CUtensorMap& c, BwArgs& a, bool bf16, cudaStream_t s) {
     a.n_tiles = static_cast<int>((a.N + BN - 1) / BN);
     const int64_t units = static_cast<int64_t>(a.j_tiles) * a.n_tiles, nr = (a.R + BR - 1) / BR;
     int split = 1;
     while (split < 8 && units * (split + 1) <= device_sm_count() && split < nr) ++split;
     if (split > 1)
-        return bf16 ? launch<MODE, NP, BN, true, true>(m, a, split, s) : launch<MODE, NP, BN, false, true>(m, a, split, s);
-    return bf16 ? launch<MODE, NP, BN, true, false>(m, a, 1, s) : launch<MODE, NP, BN, false, false>(m, a, 1, s);
+        return bf16 ? launch<MODE, NP, BN, true, true>(m, c, a, split, s) : launch<MODE, NP, BN, false, true>(m, c, a, split, s);
+    return bf16 ? launch<MODE, NP, BN, true, false>(m, c, a, 1, s) : launch<MODE, NP, BN, false, false>(m, c, a, 1, s);
 }
 
 template <int NP>
 cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, cudaStream_t s) {
-    CUtensorMap m;
+    CUtensorMap m, c;
     const int bn = a.N <= 32 ? 32 : a.N <= 64 ? 64 : a.N <= 128 ? 128 : 256;
-    const cudaError_t e = make_x_map(&m, dY, a.R, a.N, ldd, bn);
+    cudaError_t e = make_x_map(&m, dY, a.R, a.N, ldd, bn);
+    if (e == cudaSuccess) e = make_planes_map(&c, a, NP);
     if (e != cudaSuccess) return e;
     switch (bn) {
-        case 32: return launch_bn<DGRAD, NP, 32>(m, a, bf16, s);
-        case 64: return launch_bn<DGRAD, NP, 64>(m, a, bf16, s);
-        case 128: return launch_bn<DGRAD, NP, 128>(m, a, bf16, s);
-        default: return launch_bn<DGRAD, NP, 256>(m, a, bf16, s);
+        case 32: return launch_bn<DGRAD, NP, 32>(m, c, a, bf16, s);
+        case 64: return launch_bn<DGRAD, NP, 64>(m, c, a, bf16, s);
+        case 128: return launch_bn<DGRAD, NP, 128>(m, c, a, bf16, s);
+        default: return launch_bn<DGRAD, NP, 256>(m, c, a, bf16, s);
     }
 }
 
@@ -532,12 +671,13 @@ cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M,
     a.ldo = ldw;
     a.j_tiles = static_cast<int>(K / 128);
     a.out_dt = dw_dt;
-    CUtensorMap m;
-    const cudaError_t e = make_x_map(&m, dY, M, T, ldd, BR);      // boxes of 64 m x 64 t
+    CUtensorMap m, c;
+    cudaError_t e = make_x_map(&m, dY, M, T, ldd, BR);      // boxes of 64 m x 64 t
+    if (e == cudaSuccess) e = make_x8_map(&c, codes, K, T, 1, BR);
     if (e != cudaSuccess) return e;
-    if (M <= 64) return launch_bn<WGRAD, 1, 64>(m, a, bf16, s);
-    if (M <= 128) return launch_bn<WGRAD, 1, 128>(m, a, bf16, s);
-    return launch_bn<WGRAD, 1, 256>(m, a, bf16, s);
+    if (M <= 64) return launch_bn<WGRAD, 1, 64>(m, c, a, bf16, s);
+    if (M <= 128) return launch_bn<WGRAD, 1, 128>(m, c, a, bf16, s);
+    return launch_bn<WGRAD, 1, 256>(m, c, a, bf16, s);
 }
 
 }  // namespace rb
