@@ -445,8 +445,9 @@ RB_API rb_status rb_unpack8(const uint8_t* codes, const float* scales, int64_t r
  * x, x_scales  device, [T][K] codes and [T][K / 128] scales (block_rows = 1).
  * Y            device, out, [T][ldy] of y_dtype, ldy >= M.
  * T            1..2^22.
- * workspace    at least 256 bytes, 16-byte aligned: the header with the error
- *              word that rb_gemm_check reads. Nothing needs to be zero.
+ * workspace    nullable: at least 256 bytes, 16-byte aligned, the header with
+ *              the error word that rb_gemm_check reads (nothing needs to be
+ *              zero). With NULL a failure of the kernel goes unrecorded.
  * Errors: as rb_gemm.
  */
 RB_API rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t* x, const float* x_scales, int64_t M,

@@ -405,27 +405,49 @@ def dual_gemv(planes: torch.Tensor, h: torch.Tensor, g: Optional[torch.Tensor], 
 
 
 _DT8 = {torch.float32: _lib.RB_F32, torch.float16: _lib.RB_F16, torch.bfloat16: _lib.RB_BF16}
-_HEADER_BYTES = 256     # workspace of the calls below: the header with the error word
+_E4M3 = torch.float8_e4m3fn
+_GRAD_DT = (torch.float16, torch.bfloat16)
+# A small call lasts a few microseconds on the GPU, so what surrounds it here
+# counts: the raw stream handle is taken without a Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(dev: torch.device, fn, *args) -> None:
     """fn(*args, stream) on the current stream of `dev`, whichever device is current."""
-    if torch.cuda.current_device() == dev.index:
-        check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        check(status)
 
 
-def _matrix(t: torch.Tensor, name: str, shape=None, dtypes=None) -> torch.Tensor:
-    """t, if it is a 2-D tensor with unit column stride and a row pitch that covers its columns."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must be a 2-D tensor" + (f" of shape {shape}" if shape else ""))
+def _cuda_device(*ts: Optional[torch.Tensor]) -> torch.device:
+    """The one CUDA device that all tensors given are on."""
+    dev = None
+    for t in ts:
+        if t is not None:
+            d = t.device
+            if dev is None:
+                if d.type != "cuda":
+                    raise ValueError("tensors must live on a CUDA device")
+                dev = d
+            elif d != dev:
+                raise ValueError("tensors must live on one CUDA device")
+    return dev
+
+
+def _matrix(t: torch.Tensor, name: str, shape=None, dtypes=None) -> None:
+    """Refuses t unless it is a 2-D tensor with unit column stride and rows that do not overlap."""
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be a 2-D tensor" + (f" of shape {tuple(shape)}" if shape else ""))
     if dtypes is not None and t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}")
-    if (t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+    if not t.is_contiguous() and ((t.stride(1) != 1 and t.shape[1] > 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
         raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
-    return t
 
 
 def _pitch(t: torch.Tensor) -> int:
@@ -436,7 +458,7 @@ def _pitch(t: torch.Tensor) -> int:
 
 def _blocks8(codes: torch.Tensor, scales: torch.Tensor, block_rows: int, what: str):
     """(rows, K) of e4m3 codes [rows, K] with fp32 scales [ceil(rows / block_rows), K / 128]."""
-    if codes.dim() != 2 or codes.dtype != torch.float8_e4m3fn or not codes.is_contiguous():
+    if codes.dtype != _E4M3 or codes.dim() != 2 or not codes.is_contiguous():
         raise ValueError(f"{what}: codes must be contiguous float8_e4m3fn [rows, K]")
     rows, K = codes.shape
     if block_rows not in (1, 128):
@@ -444,15 +466,18 @@ def _blocks8(codes: torch.Tensor, scales: torch.Tensor, block_rows: int, what: s
     if K % 128:
         raise ValueError(f"{what}: K={K} is not a multiple of 128")
     shape = (-(-rows // block_rows), K // 128)
-    if tuple(scales.shape) != shape or scales.dtype != torch.float32 or not scales.is_contiguous():
+    if scales.shape != shape or scales.dtype != torch.float32 or not scales.is_contiguous():
         raise ValueError(f"{what}: scales must be contiguous fp32 of shape {shape}")
     return rows, K
 
 
-def _header(workspace: Optional[torch.Tensor], dev: torch.device) -> torch.Tensor:
-    if workspace is None or workspace.numel() * workspace.element_size() < _HEADER_BYTES:
-        return torch.empty(_HEADER_BYTES, dtype=torch.uint8, device=dev)
-    return workspace
+def _header(workspace: Optional[torch.Tensor], check_device: bool, dev: torch.device):
+    """(workspace, its address, its bytes): the caller's, one for check_device, or none."""
+    if workspace is None:
+        if not check_device:
+            return None, None, 0
+        workspace = torch.empty(256, dtype=torch.uint8, device=dev)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def pack8(X: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = None,
@@ -467,19 +492,18 @@ def pack8(X: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = 
     become NaN codes and leave their block's scale alone.
     """
     lib = _lib.load()
-    dev = _require_cuda(X, codes, scales)
+    dev = _cuda_device(X, codes, scales)
     _matrix(X, "X", dtypes=_DT8)
     rows, K = X.shape
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
+    given = codes is not None or scales is not None
     if codes is None:
-        codes = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=dev)
+        codes = torch.empty((rows, K), dtype=_E4M3, device=dev)
     if scales is None:
         scales = torch.empty((-(-rows // block_rows), K // 128), dtype=torch.float32, device=dev)
-    if tuple(codes.shape) != (rows, K):
+    if given and (_blocks8(codes, scales, block_rows, "pack8") != (rows, K)):
         raise ValueError(f"codes must have shape {(rows, K)}")
-    if K % 128 == 0:        # the library refuses other K by name
-        _blocks8(codes, scales, block_rows, "pack8")
     _call(dev, lib.rb_pack8, X.data_ptr(), _DT8[X.dtype], _pitch(X), rows, K, block_rows, codes.data_ptr(),
           scales.data_ptr())
     return codes, scales
@@ -489,7 +513,7 @@ def unpack8(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 1, dtyp
             X: Optional[torch.Tensor] = None) -> torch.Tensor:
     """X = codes * scales in `dtype` (fp16, bf16 or fp32; X's own where X is given)."""
     lib = _lib.load()
-    dev = _require_cuda(codes, scales, X)
+    dev = _cuda_device(codes, scales, X)
     rows, K = _blocks8(codes, scales, block_rows, "unpack8")
     if X is None:
         if dtype not in _DT8:
@@ -509,7 +533,7 @@ def gemm8(w: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: to
     check_device=True the call waits for the stream and raises if the kernel
     recorded a failure (rb_gemm_check)."""
     lib = _lib.load()
-    dev = _require_cuda(w, w_scales, x, x_scales, Y, workspace)
+    dev = _cuda_device(w, w_scales, x, x_scales, Y, workspace)
     M, K = _blocks8(w, w_scales, 128, "w")
     T, Kx = _blocks8(x, x_scales, 1, "x")
     if Kx != K:
@@ -519,11 +543,11 @@ def gemm8(w: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: to
             raise ValueError(f"y_dtype {y_dtype}")
         Y = torch.empty((T, M), dtype=y_dtype, device=dev)
     _matrix(Y, "Y", (T, M), _DT8)
-    workspace = _header(workspace, dev)
+    workspace, ws, ws_bytes = _header(workspace, check_device, dev)
     _call(dev, lib.rb_gemm8, w.data_ptr(), w_scales.data_ptr(), x.data_ptr(), x_scales.data_ptr(), M, K, T, Y.data_ptr(),
-          _DT8[Y.dtype], max(_pitch(Y), M), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+          _DT8[Y.dtype], _pitch(Y), ws, ws_bytes)
     if check_device:
-        _call(dev, lib.rb_gemm_check, workspace.data_ptr())
+        _call(dev, lib.rb_gemm_check, ws)
     return Y
 
 
@@ -538,9 +562,9 @@ def gemm_wgrad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, add:
     checkpoint of a tensor of that type), sums are fp32 and dW is rounded once.
     """
     lib = _lib.load()
-    dev = _require_cuda(dY, codes, scales, add, dW, workspace)
+    dev = _cuda_device(dY, codes, scales, add, dW, workspace)
     T, K = _blocks8(codes, scales, 1, "checkpoint")
-    _matrix(dY, "dY", dtypes=(torch.float16, torch.bfloat16))
+    _matrix(dY, "dY", dtypes=_GRAD_DT)
     if dY.shape[0] != T:
         raise ValueError("dY and the checkpoint disagree on the number of tokens")
     M = dY.shape[1]
@@ -554,12 +578,11 @@ def gemm_wgrad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, add:
         _matrix(add, "add", (M, K), (dW.dtype,))
         if _pitch(add) != _pitch(dW):
             raise ValueError("add must have dW's row pitch")
-    workspace = _header(workspace, dev)
+    workspace, ws, ws_bytes = _header(workspace, check_device, dev)
     _call(dev, lib.rb_gemm_wgrad, dY.data_ptr(), _DT8[dY.dtype], _pitch(dY), M, codes.data_ptr(), scales.data_ptr(), K, T,
-          0 if add is None else add.data_ptr(), dW.data_ptr(), _DT8[dW.dtype], _pitch(dW), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+          None if add is None else add.data_ptr(), dW.data_ptr(), _DT8[dW.dtype], _pitch(dW), ws, ws_bytes)
     if check_device:
-        _call(dev, lib.rb_gemm_check, workspace.data_ptr())
+        _call(dev, lib.rb_gemm_check, ws)
     return dW
 
 
@@ -571,14 +594,14 @@ def gemm_dgrad(planes: torch.Tensor, alpha: torch.Tensor, dY: torch.Tensor, K: i
     [T, M]. K is the layer's input width (sliced planes are padded to 512
     columns, so they do not say it)."""
     lib = _lib.load()
-    dev = _require_cuda(planes, alpha, dY, dX, workspace)
+    dev = _cuda_device(planes, alpha, dY, dX, workspace)
     N, M, order = _planes_geometry(planes, K)
     if planes.dtype != torch.int32 or not planes.is_contiguous():
         raise ValueError("planes must be contiguous int32")
     G = K if group == 0 else group
     if alpha.dtype not in _DT or tuple(alpha.shape) != (N, M, K // G) or not alpha.is_contiguous():
         raise ValueError(f"alpha must be contiguous fp16 or fp32 of shape {(N, M, K // G)}")
-    _matrix(dY, "dY", dtypes=(torch.float16, torch.bfloat16))
+    _matrix(dY, "dY", dtypes=_GRAD_DT)
     if dY.shape[1] != M:
         raise ValueError("dY must have M columns")
     T = dY.shape[0]
@@ -587,10 +610,9 @@ def gemm_dgrad(planes: torch.Tensor, alpha: torch.Tensor, dY: torch.Tensor, K: i
             raise ValueError(f"dx_dtype {dx_dtype}")
         dX = torch.empty((T, K), dtype=dx_dtype, device=dev)
     _matrix(dX, "dX", (T, K), _DT8)
-    workspace = _header(workspace, dev)
+    workspace, ws, ws_bytes = _header(workspace, check_device, dev)
     _call(dev, lib.rb_gemm_dgrad, planes.data_ptr(), alpha.data_ptr(), _DT[alpha.dtype], layout(M, K, N, group, order),
-          dY.data_ptr(), _DT8[dY.dtype], _pitch(dY), T, dX.data_ptr(), _DT8[dX.dtype], _pitch(dX), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+          dY.data_ptr(), _DT8[dY.dtype], _pitch(dY), T, dX.data_ptr(), _DT8[dX.dtype], _pitch(dX), ws, ws_bytes)
     if check_device:
-        _call(dev, lib.rb_gemm_check, workspace.data_ptr())
+        _call(dev, lib.rb_gemm_check, ws)
     return dX

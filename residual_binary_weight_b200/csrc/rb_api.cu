@@ -47,6 +47,17 @@ int device_sm_count() {
     return cache[dev];
 }
 
+cudaError_t allow_smem(const void* kernel, size_t bytes, SmemMark& mark) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < SmemMark::DEVICES;
+    if (known && mark.bytes[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && known) mark.bytes[dev].store(static_cast<uint32_t>(bytes), std::memory_order_release);
+    return e;
+}
+
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 static rb_status check_layout(const rb_layout& L) {
@@ -81,12 +92,16 @@ static rb_status check_blocks8(int64_t rows, int64_t K, const char* what) {
     return RB_OK;
 }
 
+// the header of the calls that can do without one
 static rb_status check_header(const void* workspace, size_t ws_bytes) {
-    if (!workspace || ws_bytes < GEMM_HEADER_BYTES || !aligned16(workspace))
+    if (!workspace) return RB_OK;
+    if ( ws_bytes < GEMM_HEADER_BYTES || !aligned16(workspace))
         return fail(RB_ERR_WORKSPACE, "workspace needs %zu bytes (16-byte aligned), got %zu", (size_t)GEMM_HEADER_BYTES,
                     ws_bytes);
     return RB_OK;
 }
+
+static uint32_t* error_word(void* workspace) { return workspace ? static_cast<uint32_t*>(workspace) + 1 : nullptr; }
 
 static rb_status launched(cudaError_t e, const char* who) {
     if (e == cudaErrorNotSupported) return fail(RB_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
@@ -535,7 +550,7 @@ rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t* x, co
     if ((st = check_header(workspace, ws_bytes)) != RB_OK) return st;
     if (static_cast<double>((T + 127) / 128) * static_cast<double>((M + 127) / 128) >= 268435456.0)
         return fail(RB_ERR_UNSUPPORTED, "T=%d x M=%lld: 2^28 tiles or more", T, (long long)M);
-    return launched(launch_gemm8(w, w_scales, x, x_scales, M, K, T, Y, y_dtype, ldy, static_cast<uint32_t*>(workspace) + 1,
+    return launched(launch_gemm8(w, w_scales, x, x_scales, M, K, T, Y, y_dtype, ldy, error_word(workspace),
                                  static_cast<cudaStream_t>(stream)),
                     "rb_gemm8 launch");
 }
@@ -568,7 +583,7 @@ rb_status rb_gemm_wgrad(const void* dY, rb_dtype dy_dtype, int64_t ldd, int64_t 
         return fail(RB_ERR_ALIGNMENT, "codes must be 16-byte aligned, scales 4-byte aligned");
     if (reinterpret_cast<uintptr_t>(add) & (dtype8_size(dw_dtype) - 1)) return fail(RB_ERR_ALIGNMENT, "add misaligned");
     return launched(launch_gemm_wgrad(dY, dy_dtype == RB_BF16, ldd, M, codes, scales, K, T, add, dW, dw_dtype, ldw,
-                                      static_cast<uint32_t*>(workspace) + 1, static_cast<cudaStream_t>(stream)),
+                                      error_word(workspace), static_cast<cudaStream_t>(stream)),
                     "rb_gemm_wgrad launch");
 }
 
@@ -587,7 +602,7 @@ rb_status rb_gemm_dgrad(const uint32_t* planes, const void* alpha, rb_dtype alph
         return fail(RB_ERR_ALIGNMENT, "alpha misaligned for its dtype");
     return launched(launch_gemm_dgrad(planes, alpha, alpha_dtype == RB_F16, L.M, L.K, L.n_paths, L.group,
                                       L.order == RB_SLICED, dY, dy_dtype == RB_BF16, ldd, T, dX, dx_dtype, ldx,
-                                      static_cast<uint32_t*>(workspace) + 1, static_cast<cudaStream_t>(stream)),
+                                      error_word(workspace), static_cast<cudaStream_t>(stream)),
                     "rb_gemm_dgrad launch");
 }
 

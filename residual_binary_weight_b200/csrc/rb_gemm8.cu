@@ -44,6 +44,9 @@ struct G8Args {
     bool y_vec;             // y rows take 16-byte stores
 };
 
+// error word of the calls without a workspace: nobody reads it
+__device__ uint32_t unrecorded;
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -145,7 +148,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     auto acc_empty = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + 2 + b); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t* err = a.err;
+    uint32_t* err = a.err ? a.err : &unrecorded;
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;      // flags are raised only by waits that ran out
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
@@ -313,7 +316,8 @@ template <int BN, bool SPLIT>
 cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& wm, const G8Args& a, unsigned grid, unsigned cluster,
                    size_t smem, cudaStream_t s) {
     auto kern = gemm8_kernel<BN, SPLIT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static SmemMark mark;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, mark);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);

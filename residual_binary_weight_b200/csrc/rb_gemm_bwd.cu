@@ -18,8 +18,8 @@
 // per path); A, its expansion; B, the dY tiles. The expansion only waits for
 // C and for a free slot of A, so neither load's latency meets it.
 //
-// Roles (480 threads): warps 0-3 epilogue, 4-11 expansion in two groups that
-// take the stages in turn, 12 B loads, 13 MMAs, 14 C loads.
+// Roles: warps 0-3 epilogue, then two or three groups of four expansion warps
+// that take the stages in turn, and one warp each for B loads, MMAs and C loads.
 // A CTA walks its tiles with two accumulators, so the epilogue of a tile
 // overlaps the next tile's MMAs. Few tiles: a cluster of CTAs shares a
 // tile, each takes part of the rows r, and the sums meet in distributed
@@ -40,9 +40,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int EPI_WARPS = 4, EXP_WARP0 = 4, GROUP_WARPS = 4, GROUPS = 2;
-constexpr int B_WARP = 12, MMA_WARP = 13, C_WARP = 14;
-constexpr int THREADS = 480;
+constexpr int EPI_WARPS = 4, EXP_WARP0 = 4, GROUP_WARPS = 4;
 constexpr int BR = 64;                          // rows r per stage
 constexpr uint32_t A_BYTES = 128 * BR * 2;      // two chunks of [64 r][64 j]
 constexpr uint32_t CHUNK = 64 * BR * 2;         // 8 KB
@@ -52,7 +50,11 @@ template <int MODE, int NP, int BN>
 struct BwCfg {
     static constexpr uint32_t B_BYTES = BN * BR * 2;
     static constexpr uint32_t C_BYTES = MODE == WGRAD ? 128 * BR : NP * 16 * BR;
-    static constexpr int AS = 3, BS = BN >= 256 ? 4 : 6, CS = MODE == WGRAD ? 5 : 6;
+    // expansion groups: a stage's MMAs take 2 BN cycles, a group's stage about 1000
+    static constexpr int GROUPS = BN >= 256 ? 2 : 3;
+    static constexpr int B_WARP = EXP_WARP0 + GROUPS * GROUP_WARPS, MMA_WARP = B_WARP + 1, C_WARP = B_WARP + 2;
+    static constexpr int THREADS = 32 * (C_WARP + 1);
+    static constexpr int AS = BN >= 256 ? 3 : 4, BS = BN >= 256 ? 4 : 6, CS = MODE == WGRAD ? 5 : 6;
     static constexpr uint32_t TILES = AS * A_BYTES + BS * B_BYTES + CS * C_BYTES;
     static constexpr int BARS = 2 * (AS + BS + CS) + 4;
     // at least 120 KB, so that two CTAs never share an SM's tensor memory
@@ -86,6 +88,9 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// error word of the calls without a workspace: nobody reads it
+__device__ uint32_t unrecorded;
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -135,30 +140,45 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
-// The scales of one row r of the compressed operand (0 past the last row, so
-// that the row adds nothing), read ahead of the row's stage.
-template <int MODE, int NP>
-struct Scales {
-    float v[NP];
-    __device__ __forceinline__ void load(const BwArgs& a, int64_t r, int64_t j) {
+// Walks the scales of a thread's two rows per stage, UROWS apart, stage after
+// stage of its group (0 past the last row, so that the row adds nothing).
+template <int MODE, int NP, int UROWS, int STEP>
+struct ScaleWalk {
+    const char* at;
+    int64_t path, row;       // bytes between paths and between rows
+    int64_t left;            // rows from the first of the two to the end
+    bool f16;
+    __device__ __forceinline__ void start(const BwArgs& a, int64_t r, int64_t jt) {
+        const int es = MODE == DGRAD && a.alpha_f16 ? 2 : 4;
+        const bool per_block = MODE == WGRAD || a.g128;
+        row = (per_block ? a.J >> 7 : 1) * es;
+        path = a.R * row;
+        at = static_cast<const char*>(MODE == WGRAD ? static_cast<const void*>(a.scales) : a.alpha) + r * row + (per_block ? jt * es : 0);
+        left = a.R - r;
+        f16 = es == 2;
+    }
+    __device__ __forceinline__ void load(float (&v)[2][NP]) {
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            v[p] = 0.0f;
-            if (r < a.R) {
-                if constexpr (MODE == WGRAD) {
-                    v[p] = __ldg(a.scales + r * (a.J >> 7) + (j >> 7));
-                } else {
-                    const int64_t i = p * a.R + r, at = a.g128 ? i * (a.J >> 7) + (j >> 7) : i;
-                    v[p] = a.alpha_f16 ? __half2float(__ldg(static_cast<const __half*>(a.alpha) + at))
-                                       : __ldg(static_cast<const float*>(a.alpha) + at);
-                }
+        for (int k = 0; k < 2; ++k) {
+            const bool in = left > k * UROWS;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const char* q = at + k * UROWS * row + p * path;
+                v[k][p] = 0.0f;
+                if (in) v[k][p] = f16 ? __half2float(__ldg(reinterpret_cast<const __half*>(q))) : __ldg(reinterpret_cast<const float*>(q));
             }
         }
+        at += STEP * row;
+        left -= STEP;
     }
 };
 
 // 32 weights sum_p +-al_p from the 32 bits of w[p]: path 0 gives the sign, the
 // paths that agree or disagree with it choose one of 2^(NP-1) magnitudes.
+// h[i] holds columns i and i + 16 of the word: a left shift by 15 - i puts both
+// sign bits in place, and a byte's top bit spread over 16 bits by PRMT gives
+// both choices at once. The columns of a tile are thus permuted within 32
+// (position 2i: column i, 2i + 1: column i + 16), which the epilogue undoes.
 template <int NP, bool BF16>
 __device__ __forceinline__ void expand_planes(const uint32_t (&w)[NP], const float (&al)[NP], uint32_t (&h)[16]) {
     constexpr int NM = 1 << (NP - 1);
@@ -170,29 +190,28 @@ __device__ __forceinline__ void expand_planes(const uint32_t (&w)[NP], const flo
         for (int p = 1; p < NP; ++p) v += (m >> (p - 1)) & 1 ? al[p] : -al[p];
         mag[m] = pack2<BF16>(v, v);
     }
+    const uint32_t minus = ~w[0];
     uint32_t s[NP][8];
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        const uint32_t x = p == 0 ? w[0] : ~(w[0] ^ w[p]);
+    for (int p = 1; p < NP; ++p) {
+        const uint32_t x = minus ^ w[p];       // set: the path agrees with path 0
 #pragma unroll
         for (int k = 0; k < 8; ++k) s[p][k] = x << (7 - k);
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        // columns 2i and 2i+1: bit 8b + 2m (+ 1) is the top bit of byte b of s[2m (+ 1)]
-        const int m = i & 3, b = i >> 2;
-        const uint32_t lo = 8u | b, hi = 8u | (4u + b);
         uint32_t v[NM];
 #pragma unroll
         for (int k = 0; k < NM; ++k) v[k] = mag[k];
 #pragma unroll
         for (int p = 1; p < NP; ++p) {
-            const uint32_t mask = prmt(s[p][2 * m], s[p][2 * m + 1], lo | (lo << 4) | (hi << 8) | (hi << 12));
+            // bits i and i + 16: the top bits of bytes i / 8 and i / 8 + 2 of s[i % 8]
+            const uint32_t lo = 8u | (i >> 3), hi = 8u | ((i >> 3) + 2);
+            const uint32_t mask = prmt(s[p][i & 7], 0u, lo | (lo << 4) | (hi << 8) | (hi << 12));
 #pragma unroll
             for (int k = 0; k < (NM >> p); ++k) v[k] = (mask & v[2 * k + 1]) | (~mask & v[2 * k]);
         }
-        const uint32_t sgn = prmt(s[0][2 * m], s[0][2 * m + 1], (lo << 4) | (hi << 12));
-        h[i] = v[0] ^ (~sgn & 0x80008000u);
+        h[i] = v[0] ^ ((minus << (15 - i)) & 0x80008000u);
     }
 }
 
@@ -289,10 +308,11 @@ __device__ __forceinline__ void store_rows(void* out, const void* add, int64_t a
 }
 
 template <int MODE, int NP, int BN, bool BF16, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(BwCfg<MODE, NP, BN>::THREADS, 1)
 gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap cmap, BwArgs a) {
     using C = BwCfg<MODE, NP, BN>;
-    constexpr int AS = C::AS, BS = C::BS, CS = C::CS;
+    constexpr int AS = C::AS, BS = C::BS, CS = C::CS, GROUPS = C::GROUPS;
+    constexpr int B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP;
     extern __shared__ __align__(1024) unsigned char dsm[];
     __shared__ __align__(8) uint64_t bars[C::BARS];
     __shared__ uint32_t tmem_slot;
@@ -313,7 +333,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     auto acc_empty = [&](int b) { return bar0 + 8u * (2 * (AS + BS + CS) + 2 + b); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t* err = a.err;
+    uint32_t* err = a.err ? a.err : &unrecorded;
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;      // flags are raised only by waits that ran out
     if (threadIdx.x == 0) {
         for (int s = 0; s < AS; ++s) {
@@ -438,30 +458,37 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         if (!ok)
             for (int i = tile - 1; i >= 0 && i >= tile - 2; --i) mbar_drain(acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u);
     } else if (warp >= EXP_WARP0) {
-        const int grp = (warp - EXP_WARP0) / GROUP_WARPS, wd = (warp - EXP_WARP0) % GROUP_WARPS;
-        const uint32_t sw = static_cast<uint32_t>(lane & 7);
-        // this thread's rows of a stage are lane and lane + 32, its columns 32 wd .. 32 wd + 31
-        const uint32_t at = static_cast<uint32_t>(wd >> 1) * CHUNK + static_cast<uint32_t>(lane) * 128u;
+        // A thread expands two rows of a stage, 32 columns of each. wgrad: warp wq
+        // takes columns 32 wq.. of rows lane and lane + 32. dgrad: 4 lanes
+        // share a row (its 4 words, one LDS of 128 contiguous bytes per 8
+        // rows); the words 2 and 3 go to the other 64-column chunk, whose
+        // rows lie on the same banks, so their lanes store the 16-byte
+        // pieces in the order 2, 3, 0, 1 (bytes of the word swapped to match).
+        // Either way the 8 lanes of a store phase cover all banks once.
+        constexpr int UROWS = MODE == WGRAD ? 32 : 8;
+        const int grp = (warp - EXP_WARP0) / GROUP_WARPS, wq = (warp - EXP_WARP0) % GROUP_WARPS;
+        const int wd = MODE == WGRAD ? wq : lane & 3;
+        const uint32_t row = MODE == WGRAD ? lane : wq * 16 + (lane >> 2);
+        const uint32_t sw = row & 7u;
+        const uint32_t at = static_cast<uint32_t>(wd >> 1) * CHUNK + row * 128u;
         const uint32_t c0 = static_cast<uint32_t>(wd & 1) * 4u;
+        const uint32_t cx = MODE == DGRAD && wd >= 2 ? 2u : 0u;
+        const uint32_t bytes = cx ? 0x2301u : 0x3210u;
         Ring<AS> qa;
         Ring<CS> qc;
         bool ok = true;
-        int it = 0;                      // stages before this tile
+        int it = 0;                      // stages before this tile, modulo GROUPS
         qa.next(grp);
         qc.next(grp);
-        for (int u = u0; u < units && ok; u += u_step, it += r_hi - r_lo) {
-            const int64_t j = static_cast<int64_t>(u % a.j_tiles) * 128 + wd * 32;
-            int rb = r_lo + ((grp - it) & 1);          // the group's first stage of this tile
-            Scales<MODE, NP> cur[2], nxt[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                cur[k].load(a, static_cast<int64_t>(rb) * BR + lane + 32 * k, j);
-                nxt[k].load(a, static_cast<int64_t>(rb + GROUPS) * BR + lane + 32 * k, j);
-            }
+        for (int u = u0; u < units && ok; u += u_step, it = (it + r_hi - r_lo) % GROUPS) {
+            int rb = r_lo + (grp - it + GROUPS) % GROUPS;          // the group's first stage of this tile
+            ScaleWalk<MODE, NP, UROWS, GROUPS * BR> walk;
+            walk.start(a, static_cast<int64_t>(rb) * BR + row, u % a.j_tiles);
+            float cur[2][NP], nxt[2][NP], far[2][NP];
+            walk.load(cur);
+            walk.load(nxt);
             for (; rb < r_hi; rb += GROUPS, qa.next(GROUPS), qc.next(GROUPS)) {
-                Scales<MODE, NP> far[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) far[k].load(a, static_cast<int64_t>(rb + 2 * GROUPS) * BR + lane + 32 * k, j);
+                walk.load(far);
                 if (!__all_sync(FULL_MASK, mbar_wait(full_c(qc.slot), qc.ph, abort_flag, err, 4u))) {
                     ok = false;
                     break;
@@ -469,17 +496,18 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 uint32_t h[2][16];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t row = static_cast<uint32_t>(lane + 32 * k);
+                    const uint32_t r = row + k * UROWS;
                     if constexpr (MODE == WGRAD) {
-                        const uint32_t base = c_tile(qc.slot) + row * 128u;
+                        const uint32_t base = c_tile(qc.slot) + r * 128u;
                         const uint4 x = lds128(base + (((2u * wd) ^ sw) << 4)), y = lds128(base + (((2u * wd + 1u) ^ sw) << 4));
                         const uint32_t c[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                        expand_codes<BF16>(c, cur[k].v[0], h[k]);
+                        expand_codes<BF16>(c, cur[k][0], h[k]);
                     } else {
                         uint32_t w[NP];
 #pragma unroll
-                        for (int p = 0; p < NP; ++p) w[p] = lds32(c_tile(qc.slot) + p * 16u * BR + row * 16u + 4u * wd);
-                        expand_planes<NP, BF16>(w, cur[k].v, h[k]);
+                        for (int p = 0; p < NP; ++p)
+                            w[p] = prmt(lds32(c_tile(qc.slot) + p * 16u * BR + r * 16u + 4u * wd), 0u, bytes);
+                        expand_planes<NP, BF16>(w, cur[k], h[k]);
                     }
                 }
                 __syncwarp();
@@ -490,27 +518,30 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t base = a_tile(qa.slot) + at + static_cast<uint32_t>(k) * 4096u;
+                    const uint32_t base = a_tile(qa.slot) + at + static_cast<uint32_t>(k * UROWS) * 128u;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        sts128(base + (((c0 + c) ^ sw) << 4), h[k][4 * c], h[k][4 * c + 1], h[k][4 * c + 2], h[k][4 * c + 3]);
+                        sts128(base + (((c0 + (c ^ cx)) ^ sw) << 4), h[k][4 * c], h[k][4 * c + 1], h[k][4 * c + 2], h[k][4 * c + 3]);
                 }
                 fence_proxy_async_smem();   // make the generic-proxy stores visible to the tensor core
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full_a(qa.slot));
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    cur[k] = nxt[k];
-                    nxt[k] = far[k];
-                }
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        cur[k][p] = nxt[k][p];
+                        nxt[k][p] = far[k][p];
+                    }
             }
         }
     } else {
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+        const int column = MODE == DGRAD ? (lane >> 1) + (lane & 1) * 16 : lane;      // of this tensor-memory lane
         int tile = 0;
         for (int u = u0; u < units; u += u_step, ++tile) {
             const int b = tile & 1;
-            const int64_t j = static_cast<int64_t>(u % a.j_tiles) * 128 + warp * 32 + lane;
+            const int64_t j = static_cast<int64_t>(u % a.j_tiles) * 128 + warp * 32 + column;
             const int64_t n0 = static_cast<int64_t>(u / a.j_tiles) * BN;
             if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(tile >> 1) & 1u, abort_flag, err, 8u)) ||
                 *abort_flag)
@@ -521,7 +552,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 uint32_t v[32];
                 tmem_load<32>(tmem + lanes + static_cast<uint32_t>(b * BN + c0), v);
                 if constexpr (SPLIT) {
-                    float* buf = reinterpret_cast<float*>(dsm + (tiles - smem_addr(dsm))) + c0 * 128 + warp * 32 + lane;
+                    float* buf = reinterpret_cast<float*>(dsm + (tiles - smem_addr(dsm))) + c0 * 128 + warp * 32 + column;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) buf[i * 128] = __uint_as_float(v[i]);
                 } else {
@@ -585,12 +616,13 @@ template <int MODE, int NP, int BN, bool BF16, bool SPLIT>
 cudaError_t launch(const CUtensorMap& m, const CUtensorMap& c, BwArgs& a, int split, cudaStream_t s) {
     constexpr size_t smem = BwCfg<MODE, NP, BN>::SMEM;
     auto kern = gemm_bwd_kernel<MODE, NP, BN, BF16, SPLIT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static SmemMark mark;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, mark);
     if (e != cudaSuccess) return e;
     const int64_t units = static_cast<int64_t>(a.j_tiles) * a.n_tiles;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? units * split : std::min<int64_t>(units, device_sm_count())));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(BwCfg<MODE, NP, BN>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];

@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace rb {
 
 constexpr unsigned FULL_MASK = 0xffffffffu;
@@ -150,6 +152,15 @@ cudaError_t launch_gemm_dgrad(const uint32_t* planes, const void* alpha, bool al
                               void* dX, int dx_dt, int64_t ldx, uint32_t* err, cudaStream_t s);
 
 int device_sm_count();
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device. The
+// mark, one per kernel, remembers it: the runtime call costs more than all
+// other checks of a small launch. (Two threads may both make the call.)
+struct SmemMark {
+    static constexpr int DEVICES = 64;
+    std::atomic<uint32_t> bytes[DEVICES] = {};
+};
+cudaError_t allow_smem(const void* kernel, size_t bytes, SmemMark& mark);
 
 // Device address of the static scratch array of rb_gemv_noalloc on the
 // current device (looked up once per device).

@@ -59,7 +59,7 @@ def test_gemm8_refusals():
     assert call(T=0) == call(T=(1 << 22) + 1) == call(K=64) == "RB_ERR_UNSUPPORTED"
     assert call(w=FAKE + 4) == call(x=FAKE + 8) == call(ws=FAKE + 2) == call(xs=FAKE + 1) == "RB_ERR_ALIGNMENT"
     assert call(Y=FAKE + 1) == call(Y=FAKE + 2, dt=F32) == "RB_ERR_ALIGNMENT"
-    assert call(wk=None) == call(wb=255) == call(wk=FAKE + 8) == "RB_ERR_WORKSPACE"
+    assert call(wb=255) == call(wk=FAKE + 8) == "RB_ERR_WORKSPACE"
     assert call(T=1 << 22, M=1 << 24, K=128, ldy=1 << 24) == "RB_ERR_UNSUPPORTED"
 
 
@@ -74,7 +74,7 @@ def test_wgrad_refusals():
     assert call(T=0) == call(T=(1 << 22) + 1) == call(K=100) == "RB_ERR_UNSUPPORTED"
     assert call(ldd=100) == call(dY=FAKE + 8) == call(codes=FAKE + 8) == call(scales=FAKE + 2) == "RB_ERR_ALIGNMENT"
     assert call(dW=FAKE + 2) == call(add=FAKE + 2) == "RB_ERR_ALIGNMENT"
-    assert call(wk=None) == call(wb=0) == "RB_ERR_WORKSPACE"
+    assert call(wb=0) == "RB_ERR_WORKSPACE"
 
 
 def test_dgrad_refusals():
