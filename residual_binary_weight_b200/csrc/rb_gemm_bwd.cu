@@ -20,10 +20,19 @@
 //
 // Roles: warps 0-3 epilogue, then two or three groups of four expansion warps
 // that take the stages in turn, and one warp each for B loads, MMAs and C loads.
-// A CTA walks its tiles with two accumulators, so the epilogue of a tile
-// overlaps the next tile's MMAs. Few tiles: a cluster of CTAs shares a
-// tile, each takes part of the rows r, and the sums meet in distributed
-// shared memory in rank order.
+// Three forms:
+//   ONE    a CTA walks its 128 x BN tiles with two accumulators, so the
+//          epilogue of a tile overlaps the next tile's MMAs;
+//   SPLIT  few tiles: a cluster of CTAs shares a tile, each takes part of the
+//          rows r, and the sums meet in distributed shared memory in rank
+//          order;
+//   PAIR   256-wide n tiles: two CTAs share a 256 x 256 tile (cta_group::2);
+//          each expands its own 128 columns j and loads half of the dY tile.
+//          What bounds the kernel is shared memory's 128 bytes per cycle:
+//          one CTA writes and reads 16 KB of A and 32 KB of B (and the compressed
+//          operand) for 512 cycles of MMAs, which took 860 cycles a stage
+//          (dgrad, two paths; tensor pipe 60 %) and 1000 (wgrad; 50 %).
+//          The pair moves 16 KB of B in each CTA.
 //
 // Rounding: dgrad's operand W^[i][j] is the exact sum of the scales (to fp32)
 // rounded once to dY's 16-bit type; wgrad's operand s c is exact in that type
@@ -45,18 +54,20 @@ constexpr int BR = 64;                          // rows r per stage
 constexpr uint32_t A_BYTES = 128 * BR * 2;      // two chunks of [64 r][64 j]
 constexpr uint32_t CHUNK = 64 * BR * 2;         // 8 KB
 enum : int { DGRAD = 0, WGRAD = 1 };
+enum : int { ONE = 0, SPLIT = 1, PAIR = 2 };
 
-template <int MODE, int NP, int BN>
+template <int MODE, int NP, int BN, int FORM>
 struct BwCfg {
-    static constexpr uint32_t B_BYTES = BN * BR * 2;
+    static constexpr int BNC = FORM == PAIR ? BN / 2 : BN;      // rows of the dY tile in this CTA
+    static constexpr uint32_t B_BYTES = BNC * BR * 2;
     static constexpr uint32_t C_BYTES = MODE == WGRAD ? 128 * BR : NP * 16 * BR;
     // expansion groups: a stage's MMAs take 2 BN cycles, a group's stage about 1000
-    static constexpr int GROUPS = BN >= 256 ? 2 : 3;
+    static constexpr int GROUPS = 3;
     static constexpr int B_WARP = EXP_WARP0 + GROUPS * GROUP_WARPS, MMA_WARP = B_WARP + 1, C_WARP = B_WARP + 2;
     static constexpr int THREADS = 32 * (C_WARP + 1);
-    static constexpr int AS = BN >= 256 ? 3 : 4, BS = BN >= 256 ? 4 : 6, CS = MODE == WGRAD ? 5 : 6;
+    static constexpr int AS = BNC >= 256 ? 3 : 4, BS = BNC >= 256 ? 4 : 6, CS = MODE == WGRAD ? 5 : 6;
     static constexpr uint32_t TILES = AS * A_BYTES + BS * B_BYTES + CS * C_BYTES;
-    static constexpr int BARS = 2 * (AS + BS + CS) + 4;
+    static constexpr int BARS = 2 * (AS + BS + CS) + 4 + AS;
     // at least 120 KB, so that two CTAs never share an SM's tensor memory
     static constexpr uint32_t SMEM = (TILES < 119u * 1024u ? 119u * 1024u : TILES) + 1024u;
     static constexpr uint32_t TMEM_COLS = 2 * BN;
@@ -91,24 +102,9 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 // error word of the calls without a workspace: nobody reads it
 __device__ uint32_t unrecorded;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ float ld_cluster(uint32_t local, uint32_t rank) {
-    uint32_t addr;
+    const uint32_t addr = cluster_addr(local, rank);
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(local), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
@@ -123,9 +119,9 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr) {
 }
 
 // fp32 accumulator, A and B both fp16 or both bf16, A M-major, B K- or N-major
-__host__ __device__ constexpr uint32_t idesc_bw(int n, bool bf16, bool b_mn) {
+__host__ __device__ constexpr uint32_t idesc_bw(int n, bool bf16, bool b_mn, int m) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (1u << 15) | (b_mn ? 1u << 16 : 0u) |
-           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 // two floats in the 16-bit type of dY
@@ -154,7 +150,7 @@ struct ScaleWalk {
         row = (per_block ? a.J >> 7 : 1) * es;
         path = a.R * row;
         at = static_cast<const char*>(MODE == WGRAD ? static_cast<const void*>(a.scales) : a.alpha) + r * row + (per_block ? jt * es : 0);
-        left = a.R - r;
+        left = jt < a.j_tiles ? a.R - r : 0;
         f16 = es == 2;
     }
     __device__ __forceinline__ void load(float (&v)[2][NP]) {
@@ -307,10 +303,10 @@ __device__ __forceinline__ void store_rows(void* out, const void* add, int64_t a
     }
 }
 
-template <int MODE, int NP, int BN, bool BF16, bool SPLIT>
-__global__ void __launch_bounds__(BwCfg<MODE, NP, BN>::THREADS, 1)
+template <int MODE, int NP, int BN, bool BF16, int FORM>
+__global__ void __launch_bounds__(BwCfg<MODE, NP, BN, FORM>::THREADS, 1)
 gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap cmap, BwArgs a) {
-    using C = BwCfg<MODE, NP, BN>;
+    using C = BwCfg<MODE, NP, BN, FORM>;
     constexpr int AS = C::AS, BS = C::BS, CS = C::CS, GROUPS = C::GROUPS;
     constexpr int B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP;
     extern __shared__ __align__(1024) unsigned char dsm[];
@@ -331,6 +327,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     auto empty_c = [&](int s) { return bar0 + 8u * (2 * AS + 2 * BS + CS + s); };
     auto acc_full = [&](int b) { return bar0 + 8u * (2 * (AS + BS + CS) + b); };
     auto acc_empty = [&](int b) { return bar0 + 8u * (2 * (AS + BS + CS) + 2 + b); };
+    auto peer_full = [&](int s) { return bar0 + 8u * (2 * (AS + BS + CS) + 4 + s); };      // PAIR, even CTA
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* err = a.err ? a.err : &unrecorded;
@@ -339,6 +336,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         for (int s = 0; s < AS; ++s) {
             mbar_init(full_a(s), GROUP_WARPS);
             mbar_init(empty_a(s), 1);
+            mbar_init(peer_full(s), 1);
         }
         for (int s = 0; s < BS; ++s) {
             mbar_init(full_b(s), 1);
@@ -350,23 +348,33 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), EPI_WARPS);
+            mbar_init(acc_empty(b), FORM == PAIR ? 2 * EPI_WARPS : EPI_WARPS);
         }
         abort_word = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == MMA_WARP) tmem_alloc(smem_addr(&tmem_slot), C::TMEM_COLS);
+    if (warp == MMA_WARP) {
+        if constexpr (FORM == PAIR) tmem_alloc2(smem_addr(&tmem_slot), C::TMEM_COLS);
+        else tmem_alloc(smem_addr(&tmem_slot), C::TMEM_COLS);
+    }
     fence_before();
-    __syncthreads();
+    if constexpr (FORM == PAIR) cluster_sync();      // the peer's barriers are ready, too
+    else __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
 
-    const uint32_t rank = SPLIT ? cluster_rank() : 0u, size = SPLIT ? cluster_size() : 1u;
+    const uint32_t rank = FORM == ONE ? 0u : cluster_rank(), size = FORM == ONE ? 1u : cluster_size();
     const int64_t nr = (a.R + BR - 1) / BR;
-    const int r_lo = static_cast<int>(nr * rank / size), r_hi = static_cast<int>(nr * (rank + 1) / size);
-    const int units = a.j_tiles * a.n_tiles;
-    const int u0 = SPLIT ? blockIdx.x / size : blockIdx.x;
-    const int u_step = SPLIT ? units : gridDim.x;
+    const int r_lo = FORM == SPLIT ? static_cast<int>(nr * rank / size) : 0;
+    const int r_hi = FORM == SPLIT ? static_cast<int>(nr * (rank + 1) / size) : static_cast<int>(nr);
+    // a pair's CTAs take adjacent column tiles (of an odd number, the last
+    // pair's second CTA works on zeros and stores nothing)
+    const int jw = FORM == PAIR ? (a.j_tiles + 1) / 2 : a.j_tiles;
+    const int units = jw * a.n_tiles;
+    const int u0 = static_cast<int>(blockIdx.x / size);
+    const int u_step = FORM == SPLIT ? units : static_cast<int>(gridDim.x / size);
+    auto j_tile = [&](int u) { return FORM == PAIR ? 2 * (u % jw) + static_cast<int>(rank) : u % jw; };
+    auto n_tile = [&](int u) { return u / jw; };
 
     if (warp == B_WARP) {
         if (lane == 0) {
@@ -374,7 +382,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             int it = 0;
             bool ok = true;
             for (int u = u0; u < units && ok; u += u_step) {
-                const int nt = u / a.j_tiles;
+                const int n0 = n_tile(u) * BN + (FORM == PAIR ? static_cast<int>(rank) * C::BNC : 0);
                 for (int rb = r_lo; rb < r_hi; ++rb, ++it, q.next()) {
                     if (!mbar_wait(empty_b(q.slot), q.ph ^ 1u, abort_flag, err, 1u)) {
                         ok = false;
@@ -382,11 +390,11 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                     }
                     mbar_arrive_expect_tx(full_b(q.slot), C::B_BYTES);
                     if constexpr (MODE == DGRAD) {
-                        tma_load_2d(b_tile(q.slot), &dmap, rb * BR, nt * BN, full_b(q.slot));
+                        tma_load_2d(b_tile(q.slot), &dmap, rb * BR, n0, full_b(q.slot));
                     } else {
 #pragma unroll
-                        for (int c = 0; c < BN / 64; ++c)
-                            tma_load_2d(b_tile(q.slot) + c * CHUNK, &dmap, nt * BN + c * 64, rb * BR, full_b(q.slot));
+                        for (int c = 0; c < C::BNC / 64; ++c)
+                            tma_load_2d(b_tile(q.slot) + c * CHUNK, &dmap, n0 + c * 64, rb * BR, full_b(q.slot));
                     }
                 }
             }
@@ -394,6 +402,10 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             if (*abort_flag)
                 for (int i = it - 1; i >= 0 && i >= it - BS; --i)
                     mbar_drain(full_b(i % BS), static_cast<uint32_t>(i / BS) & 1u);
+            // the even CTA's commits also arrive here: all of them, before the CTA may go
+            else if (FORM == PAIR)
+                for (int i = it - 1; i >= 0 && i >= it - BS; --i)
+                    mbar_drain(empty_b(i % BS), static_cast<uint32_t>(i / BS) & 1u);
         }
     } else if (warp == C_WARP) {
         if (lane == 0) {
@@ -402,7 +414,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             bool ok = true;
             const int S = static_cast<int>((a.J + 511) >> 9);
             for (int u = u0; u < units && ok; u += u_step) {
-                const int jt = u % a.j_tiles;
+                const int jt = j_tile(u);
                 for (int rb = r_lo; rb < r_hi; ++rb, ++it, q.next()) {
                     if (!mbar_wait(empty_c(q.slot), q.ph ^ 1u, abort_flag, err, 1u)) {
                         ok = false;
@@ -424,18 +436,40 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 for (int i = it - 1; i >= 0 && i >= it - CS; --i)
                     mbar_drain(full_c(i % CS), static_cast<uint32_t>(i / CS) & 1u);
         }
+    } else if (FORM == PAIR && warp == MMA_WARP && rank == 1) {
+        // the pair's MMAs are issued by the even CTA: tell it, stage by stage,
+        // that this CTA's half of the operands is there
+        Ring<AS> qa;
+        Ring<BS> qb;
+        bool ok = true;
+        int it = 0;
+        for (int u = u0; u < units && ok; u += u_step) {
+            for (int rb = r_lo; rb < r_hi; ++rb, ++it, qa.next(), qb.next()) {
+                if (!__all_sync(FULL_MASK, mbar_wait(full_b(qb.slot), qb.ph, abort_flag, err, 2u) &&
+                                               mbar_wait(full_a(qa.slot), qa.ph, abort_flag, err, 2u))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_remote(peer_full(qa.slot), 0);
+                __syncwarp();
+            }
+        }
+        if (ok)
+            for (int i = it - 1; i >= 0 && i >= it - AS; --i) mbar_drain(empty_a(i % AS), static_cast<uint32_t>(i / AS) & 1u);
     } else if (warp == MMA_WARP) {
-        constexpr uint32_t idesc = idesc_bw(BN, BF16, MODE == WGRAD);
+        constexpr uint32_t idesc = idesc_bw(BN, BF16, MODE == WGRAD, FORM == PAIR ? 256 : BM);
         Ring<AS> qa;
         Ring<BS> qb;
         int tile = 0;
         bool ok = true;
         for (int u = u0; u < units && ok; u += u_step, ++tile) {
             const int b = tile & 1;
-            ok = __all_sync(FULL_MASK, mbar_wait(acc_empty(b), (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u, abort_flag, err, 2u));
+            const uint32_t aph = (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u;
+            ok = __all_sync(FULL_MASK, mbar_wait(acc_empty(b), aph, abort_flag, err, 2u));
             for (int rb = r_lo; rb < r_hi && ok; ++rb, qa.next(), qb.next()) {
                 if (!__all_sync(FULL_MASK, mbar_wait(full_b(qb.slot), qb.ph, abort_flag, err, 2u) &&
-                                               mbar_wait(full_a(qa.slot), qa.ph, abort_flag, err, 2u))) {
+                                               mbar_wait(full_a(qa.slot), qa.ph, abort_flag, err, 2u) &&
+                                               (FORM != PAIR || mbar_wait(peer_full(qa.slot), qa.ph, abort_flag, err, 2u)))) {
                     ok = false;
                     break;
                 }
@@ -443,16 +477,24 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
 #pragma unroll
                 for (int kk = 0; kk < BR / 16; ++kk) {
                     // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
+                    const uint64_t ad = smem_desc_mn(a_tile(qa.slot)) + 128u * kk;
                     const uint64_t bd = MODE == DGRAD ? smem_desc(b_tile(qb.slot)) + 2u * kk
                                                       : smem_desc_mn(b_tile(qb.slot)) + 128u * kk;
-                    umma_f16_elect(tmem + static_cast<uint32_t>(b * BN), smem_desc_mn(a_tile(qa.slot)) + 128u * kk, bd, idesc,
-                                   (rb > r_lo || kk > 0) ? 1u : 0u);
+                    const uint32_t d = tmem + static_cast<uint32_t>(b * BN), more = (rb > r_lo || kk > 0) ? 1u : 0u;
+                    if constexpr (FORM == PAIR) umma2_f16_elect(d, ad, bd, idesc, more);
+                    else umma_f16_elect(d, ad, bd, idesc, more);
                 }
-                umma_commit_elect(empty_a(qa.slot));
-                umma_commit_elect(empty_b(qb.slot));
+                if constexpr (FORM == PAIR) {
+                    umma2_commit_elect(empty_a(qa.slot));
+                    umma2_commit_elect(empty_b(qb.slot));
+                } else {
+                    umma_commit_elect(empty_a(qa.slot));
+                    umma_commit_elect(empty_b(qb.slot));
+                }
             }
             // also after an abort: the teardown waits for it
-            umma_commit_elect(acc_full(b));
+            if constexpr (FORM == PAIR) umma2_commit_elect(acc_full(b));
+            else umma_commit_elect(acc_full(b));
         }
         // every MMA issued has completed before the tensor memory is given up
         if (!ok)
@@ -483,7 +525,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         for (int u = u0; u < units && ok; u += u_step, it = (it + r_hi - r_lo) % GROUPS) {
             int rb = r_lo + (grp - it + GROUPS) % GROUPS;          // the group's first stage of this tile
             ScaleWalk<MODE, NP, UROWS, GROUPS * BR> walk;
-            walk.start(a, static_cast<int64_t>(rb) * BR + row, u % a.j_tiles);
+            walk.start(a, static_cast<int64_t>(rb) * BR + row, j_tile(u));
             float cur[2][NP], nxt[2][NP], far[2][NP];
             walk.load(cur);
             walk.load(nxt);
@@ -541,8 +583,9 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         int tile = 0;
         for (int u = u0; u < units; u += u_step, ++tile) {
             const int b = tile & 1;
-            const int64_t j = static_cast<int64_t>(u % a.j_tiles) * 128 + warp * 32 + column;
-            const int64_t n0 = static_cast<int64_t>(u / a.j_tiles) * BN;
+            const int64_t j = static_cast<int64_t>(j_tile(u)) * 128 + warp * 32 + column;
+            const int64_t n0 = static_cast<int64_t>(n_tile(u)) * BN;
+            const bool mine = FORM != PAIR || j < a.J;
             if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(tile >> 1) & 1u, abort_flag, err, 8u)) ||
                 *abort_flag)
                 break;
@@ -551,12 +594,12 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             for (int c0 = 0; c0 < BN; c0 += 32) {
                 uint32_t v[32];
                 tmem_load<32>(tmem + lanes + static_cast<uint32_t>(b * BN + c0), v);
-                if constexpr (SPLIT) {
+                if constexpr (FORM == SPLIT) {
                     float* buf = reinterpret_cast<float*>(dsm + (tiles - smem_addr(dsm))) + c0 * 128 + warp * 32 + column;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) buf[i * 128] = __uint_as_float(v[i]);
                 } else {
-                    const int left = static_cast<int>(min(static_cast<int64_t>(32), a.N - n0 - c0));
+                    const int left = mine ? static_cast<int>(min(static_cast<int64_t>(32), a.N - n0 - c0)) : 0;
                     const int64_t at = (n0 + c0) * a.ldo + j;
                     const void* add = MODE == WGRAD ? a.add : nullptr;
                     if (a.out_dt == B8_F32) store_rows<float>(a.out, add, at, a.ldo, left, v);
@@ -566,16 +609,19 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty(b));
+            if (lane == 0) {
+                if (FORM == PAIR && rank == 1) mbar_arrive_remote(acc_empty(b), 0);
+                else mbar_arrive(acc_empty(b));
+            }
         }
     }
     __syncwarp();
     fence_before();
-    if constexpr (SPLIT) {
+    if constexpr (FORM == SPLIT) {
         cluster_sync();
         // the CTAs of the cluster take the output rows in turn and add the ranks' sums in rank order
-        const int64_t j = static_cast<int64_t>(u0 % a.j_tiles) * 128 + (threadIdx.x & 127);
-        const int64_t n0 = static_cast<int64_t>(u0 / a.j_tiles) * BN;
+        const int64_t j = static_cast<int64_t>(j_tile(u0)) * 128 + (threadIdx.x & 127);
+        const int64_t n0 = static_cast<int64_t>(n_tile(u0)) * BN;
         const int rows = static_cast<int>(min(static_cast<int64_t>(BN), a.N - n0));
         if (*abort_flag == 0u && threadIdx.x < 384) {
             for (int c = static_cast<int>(rank) * 3 + (threadIdx.x >> 7); c < rows; c += static_cast<int>(size) * 3) {
@@ -587,11 +633,16 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             }
         }
         cluster_sync();      // no CTA leaves while another reads its sums
+    } else if constexpr (FORM == PAIR) {
+        cluster_sync();      // no CTA leaves while the pair's MMAs or arrivals may reach it
     } else {
         __syncthreads();
     }
     fence_after();
-    if (warp == MMA_WARP) tmem_dealloc(tmem, C::TMEM_COLS);
+    if (warp == MMA_WARP) {
+        if constexpr (FORM == PAIR) tmem_dealloc2(tmem, C::TMEM_COLS);
+        else tmem_dealloc(tmem, C::TMEM_COLS);
+    }
 }
 
 // Plane words in boxes of 4 words (one 128-column tile) x 64 rows of one path:
@@ -612,25 +663,27 @@ cudaError_t make_planes_map(CUtensorMap* map, const BwArgs& a, int n_paths) {
     return cudaSuccess;
 }
 
-template <int MODE, int NP, int BN, bool BF16, bool SPLIT>
-cudaError_t launch(const CUtensorMap& m, const CUtensorMap& c, BwArgs& a, int split, cudaStream_t s) {
-    constexpr size_t smem = BwCfg<MODE, NP, BN>::SMEM;
-    auto kern = gemm_bwd_kernel<MODE, NP, BN, BF16, SPLIT>;
+template <int MODE, int NP, int BN, bool BF16, int FORM>
+cudaError_t launch(const CUtensorMap& m, const CUtensorMap& c, BwArgs& a, int cluster, cudaStream_t s) {
+    constexpr size_t smem = BwCfg<MODE, NP, BN, FORM>::SMEM;
+    auto kern = gemm_bwd_kernel<MODE, NP, BN, BF16, FORM>;
     static SmemMark mark;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, mark);
     if (e != cudaSuccess) return e;
-    const int64_t units = static_cast<int64_t>(a.j_tiles) * a.n_tiles;
+    const int64_t units = static_cast<int64_t>(FORM == PAIR ? (a.j_tiles + 1) / 2 : a.j_tiles) * a.n_tiles;
+    const int64_t sms = device_sm_count();
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? units * split : std::min<int64_t>(units, device_sm_count())));
-    cfg.blockDim = dim3(BwCfg<MODE, NP, BN>::THREADS);
+    cfg.gridDim = dim3(static_cast<unsigned>(FORM == SPLIT ? units * cluster : FORM == PAIR ? 2 * std::min(units, sms / 2)
+                                                                                             : std::min(units, sms)));
+    cfg.blockDim = dim3(BwCfg<MODE, NP, BN, FORM>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(split);
+    at[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = SPLIT ? 1 : 0;
+    cfg.numAttrs = FORM == ONE ? 0 : 1;
     return cudaLaunchKernelEx(&cfg, kern, m, c, a);
 }
 
@@ -641,23 +694,34 @@ cudaError_t launch_bn(const CUtensorMap& m, const CUtensorMap& c, BwArgs& a, boo
     int split = 1;
     while (split < 8 && units * (split + 1) <= device_sm_count() && split < nr) ++split;
     if (split > 1)
-        return bf16 ? launch<MODE, NP, BN, true, true>(m, c, a, split, s) : launch<MODE, NP, BN, false, true>(m, c, a, split, s);
-    return bf16 ? launch<MODE, NP, BN, true, false>(m, c, a, 1, s) : launch<MODE, NP, BN, false, false>(m, c, a, 1, s);
+        return bf16 ? launch<MODE, NP, BN, true, SPLIT>(m, c, a, split, s) : launch<MODE, NP, BN, false, SPLIT>(m, c, a, split, s);
+    return bf16 ? launch<MODE, NP, BN, true, ONE>(m, c, a, 1, s) : launch<MODE, NP, BN, false, ONE>(m, c, a, 1, s);
+}
+
+// Rows of the dY tile: the narrowest that covers N; 256, as a CTA pair's, where
+// there is at least one 256 x 256 tile for each pair of SMs (otherwise more,
+// smaller tiles, or the split of their rows r, keep more SMs busy).
+int bwd_tile(const BwArgs& a) {
+    if (a.N <= 32) return 32;
+    if (a.N <= 64) return 64;
+    return a.N <= 128 || a.j_tiles * ((a.N + 127) / 128) < 2 * device_sm_count() ? 128 : 256;
 }
 
 template <int NP>
 cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, cudaStream_t s) {
     CUtensorMap m, c;
-    const int bn = a.N <= 32 ? 32 : a.N <= 64 ? 64 : a.N <= 128 ? 128 : 256;
-    cudaError_t e = make_x_map(&m, dY, a.R, a.N, ldd, bn);
+    const int bn = bwd_tile(a);
+    cudaError_t e = make_x_map(&m, dY, a.R, a.N, ldd, bn == 256 ? 128 : bn);
     if (e == cudaSuccess) e = make_planes_map(&c, a, NP);
     if (e != cudaSuccess) return e;
     switch (bn) {
         case 32: return launch_bn<DGRAD, NP, 32>(m, c, a, bf16, s);
         case 64: return launch_bn<DGRAD, NP, 64>(m, c, a, bf16, s);
         case 128: return launch_bn<DGRAD, NP, 128>(m, c, a, bf16, s);
-        default: return launch_bn<DGRAD, NP, 256>(m, c, a, bf16, s);
+        default: break;
     }
+    a.n_tiles = static_cast<int>((a.N + 255) / 256);
+    return bf16 ? launch<DGRAD, NP, 256, true, PAIR>(m, c, a, 2, s) : launch<DGRAD, NP, 256, false, PAIR>(m, c, a, 2, s);
 }
 
 }  // namespace
@@ -707,9 +771,14 @@ cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M,
     cudaError_t e = make_x_map(&m, dY, M, T, ldd, BR);      // boxes of 64 m x 64 t
     if (e == cudaSuccess) e = make_x8_map(&c, codes, K, T, 1, BR);
     if (e != cudaSuccess) return e;
-    if (M <= 64) return launch_bn<WGRAD, 1, 64>(m, c, a, bf16, s);
-    if (M <= 128) return launch_bn<WGRAD, 1, 128>(m, c, a, bf16, s);
-    return launch_bn<WGRAD, 1, 256>(m, c, a, bf16, s);
+    switch (bwd_tile(a)) {
+        case 32:
+        case 64: return launch_bn<WGRAD, 1, 64>(m, c, a, bf16, s);
+        case 128: return launch_bn<WGRAD, 1, 128>(m, c, a, bf16, s);
+        default: break;
+    }
+    a.n_tiles = static_cast<int>((M + 255) / 256);
+    return bf16 ? launch<WGRAD, 1, 256, true, PAIR>(m, c, a, 2, s) : launch<WGRAD, 1, 256, false, PAIR>(m, c, a, 2, s);
 }
 
 }  // namespace rb

@@ -243,8 +243,10 @@ def test_wgrad_any_scale_and_pitches(name):
     check_wgrad(np.random.default_rng(7), 90, 200, 384, name, any_scale=True, pad=16)
 
 
-def test_wgrad_many_tiles():
-    check_wgrad(np.random.default_rng(11), 200, 2600, 2048, "bf16", "bf16", "apart")
+@pytest.mark.parametrize("T,M,K,name,out,add", [(200, 2600, 2048, "bf16", "bf16", "apart"), (65, 4097, 1152, "f16", "f32", None),
+                                                (1, 3000, 2176, "f16", "f16", None), (330, 10000, 640, "bf16", "f32", "in place")])
+def test_wgrad_many_tiles(T, M, K, name, out, add):
+    check_wgrad(np.random.default_rng(11), T, M, K, name, out, add)
 
 
 def test_wgrad_long_sequence_few_tiles():
@@ -320,8 +322,12 @@ def test_dgrad_output_types_and_pitches(out, pad, opad):
     check_dgrad(np.random.default_rng(2), 45, 130, 256, name="bf16", out=out, pad=pad, opad=opad)
 
 
-def test_dgrad_many_tiles():
-    check_dgrad(np.random.default_rng(15), 1500, 300, 4096, order="sliced", name="bf16")
+@pytest.mark.parametrize("T,M,K,N,group,f16,order,name,out", [
+    (1500, 300, 4096, 2, 0, False, "sliced", "bf16", "bf16"), (1500, 1, 4096, 2, 0, True, "rows", "f16", "f32"),
+    (4500, 65, 1152, 1, 0, False, "rows", "f16", "f16"), (2300, 129, 2176, 3, 128, True, "sliced", "bf16", "f32"),
+    (7700, 200, 640, 4, 128, False, "rows", "f16", "bf16"), (1281, 515, 4224, 2, 128, True, "sliced", "f16", "f16")])
+def test_dgrad_many_tiles(T, M, K, N, group, f16, order, name, out):
+    check_dgrad(np.random.default_rng(15), T, M, K, N, group, f16, order, name, out)
 
 
 def test_dgrad_agrees_with_differences_of_the_forward():
