@@ -5,14 +5,36 @@
 //
 // The scales change with every 128 columns of K, so the tensor memory only
 // holds one block's product at a time: per 128 columns the MMAs write a fresh
-// 128-token x BN accumulator (two buffers in turn), and the epilogue warps
-// add sx sw times it to fp32 sums in their registers. Tokens are the MMA's M
-// (one tensor-memory lane = one thread = one token) and 128-row weight blocks
-// its N, so the factor sx sw is one register for all columns of a thread:
-// one packed fp32 FMA for two sums and no shared-memory reads.
+// accumulator (two buffers in turn), and the epilogue warps add sx sw times it
+// to fp32 sums in their registers. Tokens are the MMA's M (one tensor-memory
+// lane = one thread = one token) and weight rows its N, so the factor sx sw
+// is one register for 32 columns of a thread: one packed fp32 FMA for two
+// sums and no shared-memory reads. An epilogue warp has 32 tokens x 64
+// columns: 64 sums a thread leave room for the loads in flight, and the buffer is
+// given back as soon as the last of them has arrived, before the FMAs.
 //
-// Roles (320 threads): warps 0-7 epilogue (warp w reads the lanes of quarter
-// w % 4 and the column half w / 4), warp 8 TMA loads, warp 9 MMAs.
+// Three forms:
+//   PAIR   many tokens: two CTAs share a tile of 256 tokens x bn weight rows
+//          (cta_group::2). Each loads its 128 tokens and half of the weight
+//          rows: 32 KB written to and read from shared memory for the 512
+//          cycles of MMAs of a 128-column block, where one CTA alone
+//          would move 48 KB each way, more than its 128 bytes a cycle allow.
+//          bn is the multiple of 32 that leaves the least work in the last
+//          wave of tiles. Outputs leave through shared memory and TMA stores;
+//   SPLIT  few tiles: the K blocks of a 128 x 128 tile are divided among the
+//          CTAs of a cluster, which add their sums through distributed shared
+//          memory in rank order (two CTAs on each SM);
+//   ONE    tiles of 128 x 128 in between, two CTAs on each SM.
+//
+// The scales come through shared memory, too, eight blocks at a time: the TMA
+// warp loads a token's eight (one 32-byte sector of its row) while the eight
+// before are in use. Read by the epilogue threads themselves, block by
+// block, they cost a sector for every 4 bytes and each of the 4 column slices,
+// which took four times as long as the MMAs.
+//
+// Roles: the epilogue warps (16 in a pair's CTA, else 8; warp w reads the
+// lanes of quarter w % 4 and the columns from 64 (w / 4) on), one TMA and
+// scale warp, one MMA warp.
 #include "rb_tc.cuh"
 
 #include <cuda_bf16.h>
@@ -24,11 +46,25 @@ namespace {
 
 using namespace tc;
 
-constexpr int THREADS = 320;
-constexpr int EPI_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9;
-constexpr int TM = 128;                 // tokens per tile
+constexpr int TM = 128;                 // tokens per CTA
 constexpr uint32_t KB = 128;            // bytes of K per stage: one scale block, one swizzle row
 constexpr int MAX_STAGES = 8;
+constexpr int SG = 8;                   // K blocks whose scales are staged together
+constexpr int SLOTS = 2;
+constexpr uint32_t SLOT_FLOATS = SG * (TM + 4);      // [SG][128 tokens], then [SG][4 weight blocks]
+enum : int { ONE = 0, SPLIT = 1, PAIR = 2 };
+
+template <int FORM>
+struct G8Cfg {
+    static constexpr int EPI_WARPS = FORM == PAIR ? 16 : 8;
+    static constexpr int TMA_WARP = EPI_WARPS, MMA_WARP = EPI_WARPS + 1;
+    static constexpr int THREADS = 32 * (EPI_WARPS + 2);
+    static constexpr int BUF = FORM == PAIR ? 256 : 128;        // tensor-memory columns of a buffer
+    static constexpr uint32_t B_BYTES = 128 * KB;               // most weight rows of a CTA
+    static constexpr int CW = 16;                               // columns per tensor-memory load (registers)
+    // a pair's staged outputs: 32 rows of 128 bytes for each epilogue warp
+    static constexpr uint32_t OUT_BYTES = FORM == PAIR ? EPI_WARPS * 4096 : 0;
+};
 
 struct G8Args {
     uint32_t* err;
@@ -38,10 +74,12 @@ struct G8Args {
     int64_t M, ldy;
     int T, G;               // tokens, K / 128
     int m_tiles, n_tiles;   // token tiles, weight tiles
+    int bn;                 // weight rows per tile (PAIR: of both CTAs)
     int box;                // rows of the X box
     int stages;
     int y_dt;
-    bool y_vec;             // y rows take 16-byte stores
+    bool y_vec;             // y takes stores of 4 values at a time
+    bool y_tma;             // y takes TMA stores (PAIR)
 };
 
 // error word of the calls without a workspace: nobody reads it
@@ -57,6 +95,16 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t local, uint32_t rank) {
 }
 
 // D (+)= A x B, fp8 operands from shared memory, one elected lane of a converged warp
+__device__ __forceinline__ void umma2_f8_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
 __device__ __forceinline__ void umma_f8_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                               uint32_t accumulate) {
     asm volatile(
@@ -67,9 +115,9 @@ __device__ __forceinline__ void umma_f8_elect(uint32_t d_tmem, uint64_t adesc, u
         ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
 
-// both operands e4m3, K-major, fp32 accumulator, M = 128, N = n
-__host__ __device__ constexpr uint32_t idesc_e4m3(int n) {
-    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
+// both operands e4m3, K-major, fp32 accumulator
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 __device__ __forceinline__ void fma2(float2& acc, float a, float b, uint64_t ss) {
@@ -105,32 +153,58 @@ __device__ __forceinline__ void store4(const G8Args& a, int64_t t, int64_t m, fl
     }
 }
 
-// BN: weight rows per tile (256: two scale blocks, one per column half).
-// SPLIT: the K blocks of a tile are divided among the CTAs of a cluster,
-// which add their sums through distributed shared memory; one tile per
-// cluster. Otherwise every CTA walks the tiles by the grid's size.
-template <int BN, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, BN == 128 ? 2 : 1)
-gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap, G8Args a) {
-    constexpr int HALF = BN / 2;                       // columns of one epilogue thread
-    constexpr uint32_t B_BYTES = BN * KB;
+// two outputs as 32 bits of a 16-bit type
+__device__ __forceinline__ uint32_t pack_out(float2 v, int dt) {
+    if (dt == B8_F16) {
+        const __half2 h = __floats2half2_rn(v.x, v.y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// One lane: 32 rows of 128 staged bytes to Y (what lies past its rows or columns is not written).
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+template <int FORM>
+__global__ void __launch_bounds__(G8Cfg<FORM>::THREADS, FORM == PAIR ? 1 : 2)
+gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+             const __grid_constant__ CUtensorMap ymap, G8Args a) {
+    using C = G8Cfg<FORM>;
+    constexpr int EPI_WARPS = C::EPI_WARPS, TMA_WARP = C::TMA_WARP, MMA_WARP = C::MMA_WARP, CW = C::CW;
     extern __shared__ __align__(1024) unsigned char dsm[];
-    __shared__ __align__(8) uint64_t bars[2 * MAX_STAGES + 4];
+    __shared__ __align__(8) uint64_t bars[3 * MAX_STAGES + 4 + 2 * SLOTS];
+    __shared__ float staged[SLOTS][SLOT_FLOATS];
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t abort_word;
     volatile uint32_t* abort_flag = &abort_word;
-    const uint32_t tiles = (smem_addr(dsm) + 1023u) & ~1023u;
+    const uint32_t base = (smem_addr(dsm) + 1023u) & ~1023u;
+    const uint32_t tiles = base + C::OUT_BYTES;
     const int stages = a.stages;
-    const uint32_t a_bytes = static_cast<uint32_t>(a.box) * KB;
+    const int bnc = FORM == PAIR ? a.bn / 2 : 128;        // weight rows in this CTA
+    const uint32_t a_bytes = static_cast<uint32_t>(a.box) * KB, b_bytes = static_cast<uint32_t>(bnc) * KB;
     // the X boxes first: an MMA reads 128 rows of A; those past the box are
     // bytes of the next tiles and only reach accumulator rows of no token
     auto a_tile = [&](int s) { return tiles + static_cast<uint32_t>(s) * a_bytes; };
-    auto b_tile = [&](int s) { return tiles + static_cast<uint32_t>(stages) * a_bytes + static_cast<uint32_t>(s) * B_BYTES; };
+    auto b_tile = [&](int s) { return tiles + static_cast<uint32_t>(stages) * a_bytes + static_cast<uint32_t>(s) * C::B_BYTES; };
     const uint32_t bar0 = smem_addr(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
-    auto acc_full = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + 2 + b); };
+    auto peer_full = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + s); };      // PAIR, even CTA
+    auto acc_full = [&](int b) { return bar0 + 8u * (3 * MAX_STAGES + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (3 * MAX_STAGES + 2 + b); };
+    auto sc_full = [&](int n) { return bar0 + 8u * (3 * MAX_STAGES + 4 + n); };
+    auto sc_empty = [&](int n) { return bar0 + 8u * (3 * MAX_STAGES + 4 + SLOTS + n); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* err = a.err ? a.err : &unrecorded;
@@ -139,70 +213,182 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         for (int s = 0; s < stages; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            mbar_init(peer_full(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), EPI_WARPS);
+            mbar_init(acc_empty(b), FORM == PAIR ? 2 * EPI_WARPS : EPI_WARPS);
+        }
+        for (int n = 0; n < SLOTS; ++n) {
+            mbar_init(sc_full(n), 1);
+            mbar_init(sc_empty(n), EPI_WARPS);
         }
         abort_word = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == MMA_WARP) tmem_alloc(smem_addr(&tmem_slot), 2 * BN);
+    if (warp == MMA_WARP) {
+        if constexpr (FORM == PAIR) tmem_alloc2(smem_addr(&tmem_slot), 2 * C::BUF);
+        else tmem_alloc(smem_addr(&tmem_slot), 2 * C::BUF);
+    }
     fence_before();
-    __syncthreads();
+    if constexpr (FORM == PAIR) cluster_sync();      // the peer's barriers are ready, too
+    else __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
 
-    const uint32_t rank = SPLIT ? cluster_rank() : 0u, size = SPLIT ? cluster_size() : 1u;
-    const int g_lo = static_cast<int>(static_cast<int64_t>(a.G) * rank / size);
-    const int g_hi = static_cast<int>(static_cast<int64_t>(a.G) * (rank + 1) / size);
+    const uint32_t rank = FORM == ONE ? 0u : cluster_rank(), size = FORM == ONE ? 1u : cluster_size();
+    const int g_lo = FORM == SPLIT ? static_cast<int>(static_cast<int64_t>(a.G) * rank / size) : 0;
+    const int g_hi = FORM == SPLIT ? static_cast<int>(static_cast<int64_t>(a.G) * (rank + 1) / size) : a.G;
     const int units = a.m_tiles * a.n_tiles;
-    const int u0 = SPLIT ? blockIdx.x / size : blockIdx.x;
-    const int u_step = SPLIT ? units : gridDim.x;
+    const int u0 = static_cast<int>(blockIdx.x / size);
+    const int u_step = FORM == SPLIT ? units : static_cast<int>(gridDim.x / size);
+    // first token of this CTA and first weight row of the tile
+    auto token0 = [&](int u) { return (u % a.m_tiles) * (FORM == PAIR ? 2 * TM : TM) + (FORM == PAIR ? static_cast<int>(rank) * TM : 0); };
+    auto row0 = [&](int u) { return (u / a.m_tiles) * a.bn; };
 
+    const int w_blocks = static_cast<int>((a.M + 127) / 128);
     if (warp == TMA_WARP) {
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int u = u0; u < units && ok; u += u_step) {
-                const int mt = u % a.m_tiles, nt = u / a.m_tiles;
-                for (int g = g_lo; g < g_hi; ++g, ++it) {
-                    const int s = it % stages;
-                    if (!mbar_wait(empty_bar(s), (static_cast<uint32_t>(it / stages) & 1u) ^ 1u, abort_flag, err, 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(full_bar(s), a_bytes + B_BYTES);
-                    tma_load_3d(b_tile(s), &wmap, g * static_cast<int>(KB), nt * BN, 0, full_bar(s));
-                    tma_load_3d(a_tile(s), &xmap, g * static_cast<int>(KB), mt * TM, 0, full_bar(s));
+        // tiles: block by block, `issued` of them so far
+        int u = u0, g = g_lo, issued = 0, s = 0;
+        uint32_t ph = 1u;
+        bool ok = true;
+        auto issue_to = [&](int upto) {
+            for (; issued < upto && u < units && ok; ++issued) {
+                if (!__all_sync(FULL_MASK, mbar_wait(empty_bar(s), ph, abort_flag, err, 1u))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full_bar(s), a_bytes + b_bytes);
+                    tma_load_3d(b_tile(s), &wmap, g * static_cast<int>(KB), row0(u) + (FORM == PAIR ? static_cast<int>(rank) * bnc : 0),
+                                0, full_bar(s));
+                    tma_load_3d(a_tile(s), &xmap, g * static_cast<int>(KB), token0(u), 0, full_bar(s));
+                }
+                __syncwarp();
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++g == g_hi) {
+                    g = g_lo;
+                    u += u_step;
                 }
             }
-            // after an abort the loads in flight land before the CTA gives up its shared memory
-            if (*abort_flag)
-                for (int i = it - 1; i >= 0 && i >= it - stages; --i)
-                    mbar_drain(full_bar(i % stages), static_cast<uint32_t>(i / stages) & 1u);
+        };
+        // scales of one group of up to SG blocks: 4 tokens a lane, and a
+        // weight block's value of one K block (4 weight blocks)
+        float xr[4][SG], wr = 0.0f;
+        const bool vec = (a.G & 3) == 0 && (g_lo & 3) == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15u) == 0;
+        auto load = [&](int us, int gs) {
+            const int t0 = token0(us), n = min(SG, g_hi - gs);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = t0 + lane + 32 * k;
+                const float* p = a.xs + static_cast<int64_t>(t) * a.G + gs;
+                if (t < a.T && vec && n == SG) {
+                    const float4 lo = __ldg(reinterpret_cast<const float4*>(p)), hi = __ldg(reinterpret_cast<const float4*>(p) + 1);
+                    xr[k][0] = lo.x, xr[k][1] = lo.y, xr[k][2] = lo.z, xr[k][3] = lo.w;
+                    xr[k][4] = hi.x, xr[k][5] = hi.y, xr[k][6] = hi.z, xr[k][7] = hi.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < SG; ++i) xr[k][i] = t < a.T && i < n ? __ldg(p + i) : 0.0f;
+                }
+            }
+            const int wb = min((row0(us) >> 7) + (lane & 3), w_blocks - 1);
+            wr = (lane >> 2) < n ? __ldg(a.ws + static_cast<int64_t>(wb) * a.G + gs + (lane >> 2)) : 0.0f;
+        };
+        int done = 0, slot = 0;
+        uint32_t sph = 1u;
+        if (u0 < units) load(u0, g_lo);
+        issue_to(stages);
+        for (int us = u0; us < units && ok; us += u_step) {
+            for (int gs = g_lo; gs < g_hi && ok; gs += SG) {
+                if (!__all_sync(FULL_MASK, mbar_wait(sc_empty(slot), sph, abort_flag, err, 1u))) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < SG; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) staged[slot][i * TM + 32 * k + lane] = xr[k][i];
+                staged[slot][SG * TM + lane] = wr;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sc_full(slot));
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    sph ^= 1u;
+                }
+                if (gs + SG < g_hi) load(us, gs + SG);
+                else if (us + u_step < units) load(us + u_step, g_lo);
+                // a block's tiles may be awaited once the scales of all blocks that its
+                // slot's last user needs are out
+                done += min(SG, g_hi - gs);
+                issue_to(done + stages);
+            }
+        }
+        // after an abort the loads in flight land before the CTA gives up its shared memory
+        if (*abort_flag) {
+            for (int i = issued - 1; i >= 0 && i >= issued - stages; --i)
+                mbar_drain(full_bar(i % stages), static_cast<uint32_t>(i / stages) & 1u);
+        } else if (FORM == PAIR) {
+            // the even CTA's commits also arrive here: all of them, before the CTA may go
+            for (int i = issued - 1; i >= 0 && i >= issued - stages; --i)
+                mbar_drain(empty_bar(i % stages), static_cast<uint32_t>(i / stages) & 1u);
+        }
+    } else if (FORM == PAIR && warp == MMA_WARP && rank == 1) {
+        // the pair's MMAs are issued by the even CTA: tell it, stage by stage,
+        // that this CTA's half of the operands is there
+        int s = 0;
+        uint32_t ph = 0u;
+        bool ok = true;
+        for (int u = u0; u < units && ok; u += u_step) {
+            for (int g = g_lo; g < g_hi; ++g) {
+                if (!__all_sync(FULL_MASK, mbar_wait(full_bar(s), ph, abort_flag, err, 2u))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_remote(peer_full(s), 0);
+                __syncwarp();
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
         }
     } else if (warp == MMA_WARP) {
-        constexpr uint32_t idesc = idesc_e4m3(BN);
-        int it = 0;
+        const uint32_t idesc = idesc_e4m3(FORM == PAIR ? 2 * TM : TM, a.bn);
+        int it = 0, s = 0;
+        uint32_t ph = 0u;
         bool ok = true;
         for (int u = u0; u < units && ok; u += u_step) {
             for (int g = g_lo; g < g_hi; ++g, ++it) {
-                const int s = it % stages, b = it & 1;
-                if (!__all_sync(FULL_MASK, mbar_wait(acc_empty(b), (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u,
-                                                     abort_flag, err, 2u) &&
-                                               mbar_wait(full_bar(s), static_cast<uint32_t>(it / stages) & 1u,
-                                                         abort_flag, err, 2u))) {
+                const int b = it & 1;
+                if (!__all_sync(FULL_MASK, mbar_wait(full_bar(s), ph, abort_flag, err, 2u) &&
+                                               (FORM != PAIR || mbar_wait(peer_full(s), ph, abort_flag, err, 2u)) &&
+                                               mbar_wait(acc_empty(b), (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, abort_flag,
+                                                         err, 2u))) {
                     ok = false;
                     break;
                 }
                 fence_after();
                 const uint64_t ad = smem_desc(a_tile(s)), bd = smem_desc(b_tile(s));
+                const uint32_t d = tmem + static_cast<uint32_t>(b * C::BUF);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_f8_elect(tmem + static_cast<uint32_t>(b * BN), ad + 2u * kk, bd + 2u * kk, idesc, kk > 0);
-                umma_commit_elect(empty_bar(s));
-                umma_commit_elect(acc_full(b));
+                for (int kk = 0; kk < 4; ++kk) {
+                    if constexpr (FORM == PAIR) umma2_f8_elect(d, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0);
+                    else umma_f8_elect(d, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0);
+                }
+                if constexpr (FORM == PAIR) {
+                    umma2_commit_elect(acc_full(b));
+                    umma2_commit_elect(empty_bar(s));
+                } else {
+                    umma_commit_elect(acc_full(b));
+                    umma_commit_elect(empty_bar(s));
+                }
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
         }
         // every MMA issued has completed before the tensor memory is given up
@@ -210,103 +396,169 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         if (!ok)
             for (int i = it - 1; i >= 0 && i >= it - 2; --i) mbar_drain(acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u);
     } else {
-        const int q = warp & 3, h = warp >> 2;
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * HALF);
-        const int w_blocks = static_cast<int>((a.M + 127) / 128);
-        int it = 0;
+        const int q = warp & 3, slice = warp >> 2;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(slice * 64);
+        int it = 0, slot = 0;
+        uint32_t sph = 0u;
         bool ok = true;
         for (int u = u0; u < units && ok; u += u_step) {
-            const int mt = u % a.m_tiles, nt = u / a.m_tiles;
-            const int t = mt * TM + q * 32 + lane;
-            const bool live = mt * TM + q * 32 < a.T;         // some token of this warp's lanes exists
-            const float* xs = a.xs + static_cast<int64_t>(min(t, a.T - 1)) * a.G;
-            const int wb = min(BN == 256 ? 2 * nt + h : nt, w_blocks - 1);
-            const float* ws = a.ws + static_cast<int64_t>(wb) * a.G;
-            float2 acc[HALF / 2];
+            const int t = token0(u) + q * 32 + lane;
+            const int m0 = row0(u) + slice * 64;              // first column of this thread
+            // columns 0-31 and 32-63 of the thread lie in one weight block each (bn is a multiple of 32)
+            const int cols = min(64, a.bn - slice * 64);       // 64, 32, or none
+            const bool live = token0(u) + q * 32 < a.T && cols > 0;
+            const int w0 = (m0 >> 7) - (row0(u) >> 7), w1 = ((m0 + 32) >> 7) - (row0(u) >> 7);
+            float2 acc[32];
 #pragma unroll
-            for (int i = 0; i < HALF / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
-            float f = (live && g_lo < g_hi) ? __ldg(xs + g_lo) * __ldg(ws + g_lo) : 0.0f;
+            for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
             for (int g = g_lo; g < g_hi; ++g, ++it) {
                 const int b = it & 1;
-                const float f_now = f;
-                if (live && g + 1 < g_hi) f = __ldg(xs + g + 1) * __ldg(ws + g + 1);
+                const int gi = (g - g_lo) % SG;
+                if (gi == 0 && !__all_sync(FULL_MASK, mbar_wait(sc_full(slot), sph, abort_flag, err, 8u))) {
+                    ok = false;
+                    break;
+                }
+                const float* sc = staged[slot];
+                const float fx = sc[gi * TM + q * 32 + lane];
+                const float f0 = fx * sc[SG * TM + gi * 4 + w0], f1 = FORM == PAIR ? fx * sc[SG * TM + gi * 4 + w1] : f0;
+                if (gi == SG - 1 || g + 1 == g_hi) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sc_empty(slot));
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        sph ^= 1u;
+                    }
+                }
                 if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(it >> 1) & 1u, abort_flag, err, 8u))) {
                     ok = false;
                     break;
                 }
+                auto give_back = [&] {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (FORM == PAIR && rank == 1) mbar_arrive_remote(acc_empty(b), 0);
+                        else mbar_arrive(acc_empty(b));
+                    }
+                };
                 if (live) {
                     fence_after();
-                    uint64_t ff;
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(ff) : "f"(f_now));
+                    uint64_t ff[2];
+                    asm("mov.b64 %0, {%1, %1};" : "=l"(ff[0]) : "f"(f0));
+                    asm("mov.b64 %0, {%1, %1};" : "=l"(ff[1]) : "f"(f1));
 #pragma unroll
-                    for (int c = 0; c < HALF / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_load<32>(taddr + static_cast<uint32_t>(b * BN + c * 32), v);
+                    for (int c = 0; c < 64 / CW; ++c) {
+                        if (c * CW < cols) {
+                            uint32_t v[CW];
+                            tmem_load<CW>(taddr + static_cast<uint32_t>(b * C::BUF + c * CW), v);
+                            if ((c + 1) * CW == cols) give_back();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            fma2(acc[c * 16 + i], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), ff);
+                            for (int i = 0; i < CW / 2; ++i)
+                                fma2(acc[c * CW / 2 + i], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), ff[c * CW / 32]);
+                        }
                     }
-                    fence_before();
+                } else {
+                    give_back();
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty(b));
             }
             if (!ok) break;
-            const int64_t m0 = static_cast<int64_t>(nt) * BN + h * HALF;
-            if constexpr (SPLIT) {
+            if constexpr (FORM == SPLIT) {
                 // this CTA's sums, one row per token (132 floats apart: the
                 // lanes of a 16-byte store fall on distinct banks)
                 if (t < a.T) {
-                    float* row = reinterpret_cast<float*>(dsm + (tiles - smem_addr(dsm))) + (q * 32 + lane) * (BN + 4) + h * HALF;
+                    float* row = reinterpret_cast<float*>(dsm + (base - smem_addr(dsm))) + (q * 32 + lane) * 132 + slice * 64;
 #pragma unroll
-                    for (int i = 0; i < HALF / 4; ++i)
-                        reinterpret_cast<float4*>(row)[i] =
-                            make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+                    for (int i = 0; i < 16; ++i)
+                        reinterpret_cast<float4*>(row)[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+                }
+            } else if (FORM == PAIR && a.y_tma) {
+                if (live) {
+                    // through this warp's 32 x 128 bytes, 128-byte swizzled: 64
+                    // columns of a 16-bit type, or twice 32 of fp32
+                    const uint32_t out = base + static_cast<uint32_t>(warp) * 4096u;
+                    const uint32_t row = out + static_cast<uint32_t>(lane) * 128u, sw = static_cast<uint32_t>(lane & 7);
+                    const int t_row = token0(u) + q * 32;
+                    const bool f32 = a.y_dt == B8_F32;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if (r == 0 || (f32 && cols > 32)) {
+                            if (lane == 0) tma_store_wait_read();      // the store before has read the buffer
+                            __syncwarp();
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const uint32_t at = row + ((static_cast<uint32_t>(c) ^ sw) << 4);
+                                if (f32)
+                                    sts128(at, __float_as_uint(acc[r * 16 + 2 * c].x), __float_as_uint(acc[r * 16 + 2 * c].y),
+                                           __float_as_uint(acc[r * 16 + 2 * c + 1].x), __float_as_uint(acc[r * 16 + 2 * c + 1].y));
+                                else if (r == 0)
+                                    sts128(at, pack_out(acc[4 * c], a.y_dt), pack_out(acc[4 * c + 1], a.y_dt),
+                                           pack_out(acc[4 * c + 2], a.y_dt), pack_out(acc[4 * c + 3], a.y_dt));
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            // half a box where the slice has 32 columns of a 16-bit type
+                            if (lane == 0) {
+                                if (f32 || cols == 64) tma_store_2d(&ymap, out, m0 + r * 32, t_row);
+                            }
+                        }
+                    }
+                    if (!f32 && cols == 32 && t < a.T) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            store4(a, t, m0 + 4 * i, make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y));
+                    }
                 }
             } else if (t < a.T) {
 #pragma unroll
-                for (int i = 0; i < HALF / 4; ++i)
-                    store4(a, t, m0 + 4 * i, make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y));
+                for (int i = 0; i < 16; ++i)
+                    if (4 * i < cols)
+                        store4(a, t, m0 + 4 * i, make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y));
             }
         }
+        // the staged outputs have been read before the CTA gives up its shared memory
+        if (FORM == PAIR && lane == 0) tma_store_wait_read();
     }
     __syncwarp();
     fence_before();
-    if constexpr (SPLIT) {
+    if constexpr (FORM == SPLIT) {
         cluster_sync();
         // the cluster's CTAs take the 4-column groups of the tile in turn and
         // add the ranks' sums in rank order
-        const int mt = u0 % a.m_tiles, nt = u0 / a.m_tiles;
-        const int rows = min(TM, a.T - mt * TM);
+        const int t0 = token0(u0), rows = min(TM, a.T - t0);
         if (*abort_flag == 0u) {
-            for (int e = static_cast<int>(rank) * THREADS + threadIdx.x; e < rows * (BN / 4); e += static_cast<int>(size) * THREADS) {
-                const int r = e / (BN / 4), c = e % (BN / 4);
+            for (int e = static_cast<int>(rank) * C::THREADS + threadIdx.x; e < rows * 32; e += static_cast<int>(size) * C::THREADS) {
+                const int r = e / 32, c = e % 32;
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 for (uint32_t k = 0; k < size; ++k) {
-                    const float4 p = ld_cluster4(tiles + static_cast<uint32_t>((r * (BN + 4) + 4 * c) * 4), k);
+                    const float4 p = ld_cluster4(base + static_cast<uint32_t>((r * 132 + 4 * c) * 4), k);
                     v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
                 }
-                store4(a, mt * TM + r, static_cast<int64_t>(nt) * BN + 4 * c, v);
+                store4(a, t0 + r, static_cast<int64_t>(row0(u0)) + 4 * c, v);
             }
         }
         cluster_sync();      // no CTA leaves while another reads its sums
+    } else if constexpr (FORM == PAIR) {
+        cluster_sync();      // no CTA leaves while the pair's MMAs or arrivals may reach it
     } else {
         __syncthreads();
     }
     fence_after();
-    if (warp == MMA_WARP) tmem_dealloc(tmem, 2 * BN);
+    if (warp == MMA_WARP) {
+        if constexpr (FORM == PAIR) tmem_dealloc2(tmem, 2 * C::BUF);
+        else tmem_dealloc(tmem, 2 * C::BUF);
+    }
 }
 
-template <int BN, bool SPLIT>
-cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& wm, const G8Args& a, unsigned grid, unsigned cluster,
-                   size_t smem, cudaStream_t s) {
-    auto kern = gemm8_kernel<BN, SPLIT>;
+template <int FORM>
+cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& wm, const CUtensorMap& ym, const G8Args& a, unsigned grid,
+                   unsigned cluster, size_t smem, cudaStream_t s) {
+    auto kern = gemm8_kernel<FORM>;
     static SmemMark mark;
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, mark);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(G8Cfg<FORM>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -314,8 +566,26 @@ cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& wm, const G8Args& a
     at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = SPLIT ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, xm, wm, a);
+    cfg.numAttrs = FORM == ONE ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, xm, wm, ym, a);
+}
+
+// Y [T][M] in boxes of 128 bytes x 32 rows, 128-byte swizzled
+cudaError_t make_y_map(CUtensorMap* map, const G8Args& a) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const int es = a.y_dt == B8_F32 ? 4 : 2;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.M), static_cast<cuuint64_t>(a.T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ldy) * es};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), 32u};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUtensorMapDataType ty = a.y_dt == B8_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : a.y_dt == B8_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (enc(map, ty, 2, a.y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -334,32 +604,52 @@ cudaError_t launch_gemm8(const uint8_t* W, const float* w_scales, const uint8_t*
     a.y_dt = y_dt;
     const int es = y_dt == B8_F32 ? 4 : 2;
     a.y_vec = reinterpret_cast<uintptr_t>(Y) % (4 * es) == 0 && ldy % 4 == 0;
-    a.m_tiles = (T + TM - 1) / TM;
+    // a TMA store clips a box to the map's rows in pieces of 16 bytes: where M ends inside
+    // a piece it would write the values after it, too
+    a.y_tma = reinterpret_cast<uintptr_t>(Y) % 16 == 0 && (ldy * es) % 16 == 0 && (M * es) % 16 == 0;
     const int sms = device_sm_count();
-    const int64_t tiles256 = static_cast<int64_t>(a.m_tiles) * ((M + 255) / 256);
-    const bool wide = tiles256 >= sms;
-    const int bn = wide ? 256 : 128;
-    a.n_tiles = static_cast<int>((M + bn - 1) / bn);
-    const int64_t units = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
-    a.box = T >= TM ? TM : (T + 7) / 8 * 8;
-    CUtensorMap xm, wm;
-    cudaError_t e = make_x8_map(&xm, X, K, T, 1, a.box);
-    if (e == cudaSuccess) e = make_x8_map(&wm, W, K, M, 1, bn);
-    if (e != cudaSuccess) return e;
-    const size_t stage = (static_cast<size_t>(a.box) + bn) * KB;
-    if (wide) {
+    CUtensorMap xm, wm, ym{};
+    // a pair's tiles pay from one 256 x 256 tile per pair of SMs on
+    const int64_t pairs = sms / 2, t256 = (T + 255) / 256;
+    if (T > TM && t256 * ((M + 255) / 256) >= pairs) {
+        // weight rows per tile: the least time over all waves of tiles; a
+        // block's MMAs take 2 bn cycles, and the hand-over of a buffer about 400
+        int64_t best = 0;
+        for (int bn = 256; bn >= 128; bn -= 32) {
+            const int64_t waves = (t256 * ((M + bn - 1) / bn) + pairs - 1) / pairs, cost = waves * std::max(2 * bn, 400);
+            if (best == 0 || cost < best) {
+                best = cost;
+                a.bn = bn;
+            }
+        }
+        a.m_tiles = static_cast<int>(t256);
+        a.n_tiles = static_cast<int>((M + a.bn - 1) / a.bn);
+        a.box = TM;
         a.stages = 4;
-        // every MMA of the last stage reads 128 rows of A
-        return launch<256, false>(xm, wm, a, static_cast<unsigned>(std::min<int64_t>(units, sms)), 1,
-                                  1024 + a.stages * stage, s);
+        cudaError_t e = make_x8_map(&xm, X, K, T, 1, TM);
+        if (e == cudaSuccess) e = make_x8_map(&wm, W, K, M, 1, a.bn / 2);
+        if (e == cudaSuccess && a.y_tma) e = make_y_map(&ym, a);
+        if (e != cudaSuccess) return e;
+        using C = G8Cfg<PAIR>;
+        const size_t smem = 1024 + C::OUT_BYTES + static_cast<size_t>(a.stages) * (TM * KB + C::B_BYTES);
+        return launch<PAIR>(xm, wm, ym, a, static_cast<unsigned>(2 * std::min<int64_t>(pairs, t256 * a.n_tiles)), 2, smem, s);
     }
+    a.bn = 128;
+    a.m_tiles = (T + TM - 1) / TM;
+    a.n_tiles = static_cast<int>((M + 127) / 128);
+    a.box = T >= TM ? TM : (T + 7) / 8 * 8;
+    cudaError_t e = make_x8_map(&xm, X, K, T, 1, a.box);
+    if (e == cudaSuccess) e = make_x8_map(&wm, W, K, M, 1, 128);
+    if (e != cudaSuccess) return e;
+    const int64_t units = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
     // two CTAs share an SM: what fits in half of its shared memory
-    a.stages = static_cast<int>(std::min<size_t>(MAX_STAGES, (108 * 1024) / stage));
+    const size_t stage = static_cast<size_t>(a.box) * KB + 128 * KB;
+    a.stages = static_cast<int>(std::min<size_t>(MAX_STAGES, (102 * 1024) / stage));
     int split = 1;
     while (split < 8 && units * (split + 1) <= 2 * sms && split < a.G) ++split;
     const size_t smem = 1024 + std::max<size_t>(a.stages * stage, split > 1 ? static_cast<size_t>(std::min(T, TM)) * 132 * 4 : 0);
-    if (split > 1) return launch<128, true>(xm, wm, a, static_cast<unsigned>(units * split), split, smem, s);
-    return launch<128, false>(xm, wm, a, static_cast<unsigned>(std::min<int64_t>(units, 2 * sms)), 1, smem, s);
+    if (split > 1) return launch<SPLIT>(xm, wm, ym, a, static_cast<unsigned>(units * split), split, smem, s);
+    return launch<ONE>(xm, wm, ym, a, static_cast<unsigned>(std::min<int64_t>(units, 2 * sms)), 1, smem, s);
 }
 
 }  // namespace rb

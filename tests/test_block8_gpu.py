@@ -183,9 +183,10 @@ def test_gemm8_types_pitches_and_any_scales(name, pad):
     check_gemm8(np.random.default_rng(pad), 37, 331, 512, name, pad, any_scale=True)
 
 
-@pytest.mark.parametrize("T,M,K,name", [(1280, 4001, 256, "f16"), (2500, 2048, 384, "bf16"), (70, 40000, 128, "f32")])
-def test_gemm8_many_tiles(T, M, K, name):
-    check_gemm8(np.random.default_rng(T), T, M, K, name)
+@pytest.mark.parametrize("T,M,K,name,pad", [(1280, 4001, 256, "f16", 7), (2500, 2048, 384, "bf16", 0), (70, 40000, 128, "f32", 0),
+                                            (1290, 4000, 640, "f32", 0), (300, 14336, 1152, "f16", 8), (2048, 5000, 128, "bf16", 1)])
+def test_gemm8_many_tiles(T, M, K, name, pad):
+    check_gemm8(np.random.default_rng(T), T, M, K, name, pad, any_scale=True)
 
 
 def test_gemm8_nan_codes_stay_in_their_row_and_column():
