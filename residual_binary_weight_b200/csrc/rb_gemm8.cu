@@ -8,8 +8,8 @@
 // accumulator (two buffers in turn), and the epilogue warps add sx sw times it
 // to fp32 sums in their registers. Tokens are the MMA's M (one tensor-memory
 // lane = one thread = one token) and weight rows its N, so the factor sx sw
-// is one register for 32 columns of a thread: one packed fp32 FMA for two
-// sums and no shared-memory reads. An epilogue warp has 32 tokens x 64
+// is one register for 32 columns of a thread: one FMA for a sum and no
+// shared-memory reads. An epilogue warp has 32 tokens x 64
 // columns: 64 sums a thread leave room for the loads in flight, and the buffer is
 // given back as soon as the last of them has arrived, before the FMAs.
 //
@@ -120,14 +120,6 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void fma2(float2& acc, float a, float b, uint64_t ss) {
-    uint64_t c, v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(acc.x), "f"(acc.y));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(v), "l"(ss));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(acc.x), "=f"(acc.y) : "l"(c));
-}
-
 // 4 consecutive outputs of token t from column m on
 __device__ __forceinline__ void store4(const G8Args& a, int64_t t, int64_t m, float4 v) {
     const float f[4] = {v.x, v.y, v.z, v.w};
@@ -154,12 +146,12 @@ __device__ __forceinline__ void store4(const G8Args& a, int64_t t, int64_t m, fl
 }
 
 // two outputs as 32 bits of a 16-bit type
-__device__ __forceinline__ uint32_t pack_out(float2 v, int dt) {
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi, int dt) {
     if (dt == B8_F16) {
-        const __half2 h = __floats2half2_rn(v.x, v.y);
+        const __half2 h = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
@@ -398,9 +390,19 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     } else {
         const int q = warp & 3, slice = warp >> 2;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(slice * 64);
-        int it = 0, slot = 0;
-        uint32_t sph = 0u;
+        int b = 0, slot = 0;
+        uint32_t bph = 0u, sph = 0u;
         bool ok = true;
+        // the buffer's values are in this warp's registers
+        const uint32_t to = FORM == PAIR ? cluster_addr(acc_empty(0), 0) : acc_empty(0);
+        auto give_back = [&](int buf) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (FORM == PAIR) mbar_arrive_cluster(to + 8u * buf);
+                else mbar_arrive(to + 8u * buf);
+            }
+        };
         for (int u = u0; u < units && ok; u += u_step) {
             const int t = token0(u) + q * 32 + lane;
             const int m0 = row0(u) + slice * 64;              // first column of this thread
@@ -408,60 +410,61 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             const int cols = min(64, a.bn - slice * 64);       // 64, 32, or none
             const bool live = token0(u) + q * 32 < a.T && cols > 0;
             const int w0 = (m0 >> 7) - (row0(u) >> 7), w1 = ((m0 + 32) >> 7) - (row0(u) >> 7);
-            float2 acc[32];
+            float acc[64];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
-            for (int g = g_lo; g < g_hi; ++g, ++it) {
-                const int b = it & 1;
-                const int gi = (g - g_lo) % SG;
-                if (gi == 0 && !__all_sync(FULL_MASK, mbar_wait(sc_full(slot), sph, abort_flag, err, 8u))) {
+            for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+            for (int gs = g_lo; gs < g_hi; gs += SG) {
+                if (!__all_sync(FULL_MASK, mbar_wait(sc_full(slot), sph, abort_flag, err, 8u))) {
                     ok = false;
                     break;
                 }
-                const float* sc = staged[slot];
-                const float fx = sc[gi * TM + q * 32 + lane];
-                const float f0 = fx * sc[SG * TM + gi * 4 + w0], f1 = FORM == PAIR ? fx * sc[SG * TM + gi * 4 + w1] : f0;
-                if (gi == SG - 1 || g + 1 == g_hi) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sc_empty(slot));
-                    if (++slot == SLOTS) {
-                        slot = 0;
-                        sph ^= 1u;
+                const float* sx = staged[slot] + q * 32 + lane;
+                const float* sw = staged[slot] + SG * TM;
+                const int n = min(SG, g_hi - gs);
+                float fx = sx[0], fw0 = sw[w0], fw1 = FORM == PAIR ? sw[w1] : fw0;
+                for (int gi = 0; gi < n; ++gi) {
+                    if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), bph, abort_flag, err, 8u))) {
+                        ok = false;
+                        break;
                     }
-                }
-                if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(it >> 1) & 1u, abort_flag, err, 8u))) {
-                    ok = false;
-                    break;
-                }
-                auto give_back = [&] {
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (FORM == PAIR && rank == 1) mbar_arrive_remote(acc_empty(b), 0);
-                        else mbar_arrive(acc_empty(b));
+                    const float f0 = fx * fw0, f1 = FORM == PAIR ? fx * fw1 : f0;
+                    if (gi + 1 < n) {       // the next block's, on their way meanwhile
+                        fx = sx[(gi + 1) * TM];
+                        fw0 = sw[(gi + 1) * 4 + w0];
+                        fw1 = FORM == PAIR ? sw[(gi + 1) * 4 + w1] : fw0;
                     }
-                };
-                if (live) {
-                    fence_after();
-                    uint64_t ff[2];
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(ff[0]) : "f"(f0));
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(ff[1]) : "f"(f1));
+                    if (live) {
+                        fence_after();
+                        const uint32_t from = taddr + static_cast<uint32_t>(b * C::BUF);
 #pragma unroll
-                    for (int c = 0; c < 64 / CW; ++c) {
-                        if (c * CW < cols) {
-                            uint32_t v[CW];
-                            tmem_load<CW>(taddr + static_cast<uint32_t>(b * C::BUF + c * CW), v);
-                            if ((c + 1) * CW == cols) give_back();
+                        for (int c = 0; c < 64 / CW; ++c) {
+                            if (c * CW < cols) {
+                                uint32_t v[CW];
+                                tmem_load<CW>(from + static_cast<uint32_t>(c * CW), v);
+                                if ((c + 1) * CW == cols) give_back(b);
 #pragma unroll
-                            for (int i = 0; i < CW / 2; ++i)
-                                fma2(acc[c * CW / 2 + i], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), ff[c * CW / 32]);
+                                for (int i = 0; i < CW; ++i)
+                                    acc[c * CW + i] = fmaf(__uint_as_float(v[i]), c * CW < 32 ? f0 : f1, acc[c * CW + i]);
+                            }
                         }
+                    } else {
+                        give_back(b);
                     }
-                } else {
-                    give_back();
+                    b ^= 1;
+                    if (b == 0) bph ^= 1u;
+                }
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sc_empty(slot));
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    sph ^= 1u;
                 }
             }
             if (!ok) break;
+            auto four = [&](int i) {      // columns 4 i .. 4 i + 3
+                return make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+            };
             if constexpr (FORM == SPLIT) {
                 // this CTA's sums, one row per token (132 floats apart: the
                 // lanes of a 16-byte store fall on distinct banks)
@@ -469,7 +472,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                     float* row = reinterpret_cast<float*>(dsm + (base - smem_addr(dsm))) + (q * 32 + lane) * 132 + slice * 64;
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        reinterpret_cast<float4*>(row)[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+                        reinterpret_cast<float4*>(row)[i] = four(i);
                 }
             } else if (FORM == PAIR && a.y_tma) {
                 if (live) {
@@ -487,12 +490,14 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 const uint32_t at = row + ((static_cast<uint32_t>(c) ^ sw) << 4);
-                                if (f32)
-                                    sts128(at, __float_as_uint(acc[r * 16 + 2 * c].x), __float_as_uint(acc[r * 16 + 2 * c].y),
-                                           __float_as_uint(acc[r * 16 + 2 * c + 1].x), __float_as_uint(acc[r * 16 + 2 * c + 1].y));
-                                else if (r == 0)
-                                    sts128(at, pack_out(acc[4 * c], a.y_dt), pack_out(acc[4 * c + 1], a.y_dt),
-                                           pack_out(acc[4 * c + 2], a.y_dt), pack_out(acc[4 * c + 3], a.y_dt));
+                                if (f32) {
+                                    const float4 v = four(r * 8 + c);
+                                    sts128(at, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w));
+                                } else if (r == 0) {
+                                    sts128(at, pack_out(acc[8 * c], acc[8 * c + 1], a.y_dt), pack_out(acc[8 * c + 2], acc[8 * c + 3], a.y_dt),
+                                           pack_out(acc[8 * c + 4], acc[8 * c + 5], a.y_dt),
+                                           pack_out(acc[8 * c + 6], acc[8 * c + 7], a.y_dt));
+                                }
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
@@ -505,14 +510,14 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                     if (!f32 && cols == 32 && t < a.T) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            store4(a, t, m0 + 4 * i, make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y));
+                            store4(a, t, m0 + 4 * i, four(i));
                     }
                 }
             } else if (t < a.T) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (4 * i < cols)
-                        store4(a, t, m0 + 4 * i, make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y));
+                        store4(a, t, m0 + 4 * i, four(i));
             }
         }
         // the staged outputs have been read before the CTA gives up its shared memory

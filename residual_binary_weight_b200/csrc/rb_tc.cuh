@@ -114,15 +114,20 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t local, uint32_t rank) 
     return a;
 }
 
-// Arrive on the barrier of CTA `rank` that lies where `bar` lies in this one.
-// No cluster-scope release: what such an arrival announces here is data in
+// Arrive on a barrier of the cluster (an address from cluster_addr), in
+// mbar_arrive_remote the one of CTA `rank` that lies where `bar` lies in this
+// CTA. No cluster-scope release: what such an arrival announces here is data in
 // this CTA's own shared or tensor memory, fenced towards the async proxy by
 // the threads that wrote it (or loads from tensor memory that have completed),
 // and read by the pair's MMAs on this SM; no generic access of another CTA
 // follows it. (A release at cluster scope costs a memory barrier of over
 // 1000 cycles an arrival.)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar, uint32_t rank) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(bar, rank)) : "memory");
+    mbar_arrive_cluster(cluster_addr(bar, rank));
 }
 
 __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
