@@ -412,11 +412,13 @@ _GRAD_DT = (torch.float16, torch.bfloat16)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def _call(dev: torch.device, fn, *args) -> None:
     """fn(*args, stream) on the current stream of `dev`, whichever device is current."""
     index = dev.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -491,7 +493,7 @@ def pack8(X: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = 
     those shapes may be passed in to be filled. Values that are not finite
     become NaN codes and leave their block's scale alone.
     """
-    lib = _lib.load()
+    lib = _lib._lib or _lib.load()
     dev = _cuda_device(X, codes, scales)
     _matrix(X, "X", dtypes=_DT8)
     rows, K = X.shape
@@ -499,9 +501,9 @@ def pack8(X: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = 
         raise ValueError("block_rows must be 1 or 128")
     given = codes is not None or scales is not None
     if codes is None:
-        codes = torch.empty((rows, K), dtype=_E4M3, device=dev)
+        codes = torch.empty(rows, K, dtype=_E4M3, device=dev)
     if scales is None:
-        scales = torch.empty((-(-rows // block_rows), K // 128), dtype=torch.float32, device=dev)
+        scales = torch.empty(-(-rows // block_rows), K // 128, dtype=torch.float32, device=dev)
     if given and (_blocks8(codes, scales, block_rows, "pack8") != (rows, K)):
         raise ValueError(f"codes must have shape {(rows, K)}")
     _call(dev, lib.rb_pack8, X.data_ptr(), _DT8[X.dtype], _pitch(X), rows, K, block_rows, codes.data_ptr(),
@@ -512,14 +514,15 @@ def pack8(X: torch.Tensor, block_rows: int = 1, codes: Optional[torch.Tensor] = 
 def unpack8(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torch.float16,
             X: Optional[torch.Tensor] = None) -> torch.Tensor:
     """X = codes * scales in `dtype` (fp16, bf16 or fp32; X's own where X is given)."""
-    lib = _lib.load()
+    lib = _lib._lib or _lib.load()
     dev = _cuda_device(codes, scales, X)
     rows, K = _blocks8(codes, scales, block_rows, "unpack8")
     if X is None:
         if dtype not in _DT8:
             raise ValueError(f"dtype {dtype}")
-        X = torch.empty((rows, K), dtype=dtype, device=dev)
-    _matrix(X, "X", (rows, K), _DT8)
+        X = torch.empty(rows, K, dtype=dtype, device=dev)
+    else:
+        _matrix(X, "X", (rows, K), _DT8)
     _call(dev, lib.rb_unpack8, codes.data_ptr(), scales.data_ptr(), rows, K, block_rows, X.data_ptr(), _DT8[X.dtype],
           _pitch(X))
     return X
@@ -532,7 +535,7 @@ def gemm8(w: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: to
     x, x_scales = pack8(X). Any number of tokens; any fp32 scales. With
     check_device=True the call waits for the stream and raises if the kernel
     recorded a failure (rb_gemm_check)."""
-    lib = _lib.load()
+    lib = _lib._lib or _lib.load()
     dev = _cuda_device(w, w_scales, x, x_scales, Y, workspace)
     M, K = _blocks8(w, w_scales, 128, "w")
     T, Kx = _blocks8(x, x_scales, 1, "x")
@@ -541,8 +544,9 @@ def gemm8(w: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: to
     if Y is None:
         if y_dtype not in _DT8:
             raise ValueError(f"y_dtype {y_dtype}")
-        Y = torch.empty((T, M), dtype=y_dtype, device=dev)
-    _matrix(Y, "Y", (T, M), _DT8)
+        Y = torch.empty(T, M, dtype=y_dtype, device=dev)
+    else:
+        _matrix(Y, "Y", (T, M), _DT8)
     workspace, ws, ws_bytes = _header(workspace, check_device, dev)
     _call(dev, lib.rb_gemm8, w.data_ptr(), w_scales.data_ptr(), x.data_ptr(), x_scales.data_ptr(), M, K, T, Y.data_ptr(),
           _DT8[Y.dtype], _pitch(Y), ws, ws_bytes)
@@ -561,7 +565,7 @@ def gemm_wgrad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, add:
     micro-batches. The products see X rounded to dY's type (exact for a
     checkpoint of a tensor of that type), sums are fp32 and dW is rounded once.
     """
-    lib = _lib.load()
+    lib = _lib._lib or _lib.load()
     dev = _cuda_device(dY, codes, scales, add, dW, workspace)
     T, K = _blocks8(codes, scales, 1, "checkpoint")
     _matrix(dY, "dY", dtypes=_GRAD_DT)
@@ -572,8 +576,9 @@ def gemm_wgrad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, add:
         dt = dw_dtype if add is None else add.dtype
         if dt not in _DT8:
             raise ValueError(f"dw_dtype {dt}")
-        dW = torch.empty((M, K), dtype=dt, device=dev)
-    _matrix(dW, "dW", (M, K), _DT8)
+        dW = torch.empty(M, K, dtype=dt, device=dev)
+    else:
+        _matrix(dW, "dW", (M, K), _DT8)
     if add is not None:
         _matrix(add, "add", (M, K), (dW.dtype,))
         if _pitch(add) != _pitch(dW):
@@ -593,7 +598,7 @@ def gemm_dgrad(planes: torch.Tensor, alpha: torch.Tensor, dY: torch.Tensor, K: i
     W^ = sum_k alpha_k (.) B_k taken straight from the planes, dY fp16 or bf16
     [T, M]. K is the layer's input width (sliced planes are padded to 512
     columns, so they do not say it)."""
-    lib = _lib.load()
+    lib = _lib._lib or _lib.load()
     dev = _cuda_device(planes, alpha, dY, dX, workspace)
     N, M, order = _planes_geometry(planes, K)
     if planes.dtype != torch.int32 or not planes.is_contiguous():
@@ -608,8 +613,9 @@ def gemm_dgrad(planes: torch.Tensor, alpha: torch.Tensor, dY: torch.Tensor, K: i
     if dX is None:
         if dx_dtype not in _DT8:
             raise ValueError(f"dx_dtype {dx_dtype}")
-        dX = torch.empty((T, K), dtype=dx_dtype, device=dev)
-    _matrix(dX, "dX", (T, K), _DT8)
+        dX = torch.empty(T, K, dtype=dx_dtype, device=dev)
+    else:
+        _matrix(dX, "dX", (T, K), _DT8)
     workspace, ws, ws_bytes = _header(workspace, check_device, dev)
     _call(dev, lib.rb_gemm_dgrad, planes.data_ptr(), alpha.data_ptr(), _DT[alpha.dtype], layout(M, K, N, group, order),
           dY.data_ptr(), _DT8[dY.dtype], _pitch(dY), T, dX.data_ptr(), _DT8[dX.dtype], _pitch(dX), ws, ws_bytes)

@@ -94,25 +94,23 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t local, uint32_t rank) {
     return v;
 }
 
-// D (+)= A x B, fp8 operands from shared memory, one elected lane of a converged warp
-__device__ __forceinline__ void umma2_f8_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
-}
-
-__device__ __forceinline__ void umma_f8_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+// D (+)= A x B, fp8 operands from shared memory (of one CTA, or of a pair)
+template <bool PAIRED>
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (PAIRED)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
 
 // both operands e4m3, K-major, fp32 accumulator
@@ -365,18 +363,18 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                 fence_after();
                 const uint64_t ad = smem_desc(a_tile(s)), bd = smem_desc(b_tile(s));
                 const uint32_t d = tmem + static_cast<uint32_t>(b * C::BUF);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    if constexpr (FORM == PAIR) umma2_f8_elect(d, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0);
-                    else umma_f8_elect(d, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0);
+                    for (int kk = 0; kk < 4; ++kk) umma_f8<FORM == PAIR>(d, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0);
+                    if constexpr (FORM == PAIR) {
+                        umma2_commit(acc_full(b));
+                        umma2_commit(empty_bar(s));
+                    } else {
+                        umma_commit(acc_full(b));
+                        umma_commit(empty_bar(s));
+                    }
                 }
-                if constexpr (FORM == PAIR) {
-                    umma2_commit_elect(acc_full(b));
-                    umma2_commit_elect(empty_bar(s));
-                } else {
-                    umma_commit_elect(acc_full(b));
-                    umma_commit_elect(empty_bar(s));
-                }
+                __syncwarp();
                 if (++s == stages) {
                     s = 0;
                     ph ^= 1u;

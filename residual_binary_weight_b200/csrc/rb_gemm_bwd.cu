@@ -458,6 +458,10 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             for (int i = it - 1; i >= 0 && i >= it - AS; --i) mbar_drain(empty_a(i % AS), static_cast<uint32_t>(i / AS) & 1u);
     } else if (warp == MMA_WARP) {
         constexpr uint32_t idesc = idesc_bw(BN, BF16, MODE == WGRAD, FORM == PAIR ? 256 : BM);
+        auto commit = [](uint32_t bar) {
+            if constexpr (FORM == PAIR) umma2_commit(bar);
+            else umma_commit(bar);
+        };
         Ring<AS> qa;
         Ring<BS> qb;
         int tile = 0;
@@ -474,27 +478,26 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                     break;
                 }
                 fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < BR / 16; ++kk) {
-                    // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
-                    const uint64_t ad = smem_desc_mn(a_tile(qa.slot)) + 128u * kk;
-                    const uint64_t bd = MODE == DGRAD ? smem_desc(b_tile(qb.slot)) + 2u * kk
-                                                      : smem_desc_mn(b_tile(qb.slot)) + 128u * kk;
-                    const uint32_t d = tmem + static_cast<uint32_t>(b * BN), more = (rb > r_lo || kk > 0) ? 1u : 0u;
-                    if constexpr (FORM == PAIR) umma2_f16_elect(d, ad, bd, idesc, more);
-                    else umma_f16_elect(d, ad, bd, idesc, more);
+                    for (int kk = 0; kk < BR / 16; ++kk) {
+                        // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
+                        const uint64_t ad = smem_desc_mn(a_tile(qa.slot)) + 128u * kk;
+                        const uint64_t bd = MODE == DGRAD ? smem_desc(b_tile(qb.slot)) + 2u * kk
+                                                          : smem_desc_mn(b_tile(qb.slot)) + 128u * kk;
+                        const uint32_t d = tmem + static_cast<uint32_t>(b * BN), more = (rb > r_lo || kk > 0) ? 1u : 0u;
+                        if constexpr (FORM == PAIR) umma2_f16(d, ad, bd, idesc, more);
+                        else umma_f16(d, ad, bd, idesc, more);
+                    }
+                    commit(empty_a(qa.slot));
+                    commit(empty_b(qb.slot));
+                    if (rb + 1 == r_hi) commit(acc_full(b));
                 }
-                if constexpr (FORM == PAIR) {
-                    umma2_commit_elect(empty_a(qa.slot));
-                    umma2_commit_elect(empty_b(qb.slot));
-                } else {
-                    umma_commit_elect(empty_a(qa.slot));
-                    umma_commit_elect(empty_b(qb.slot));
-                }
+                __syncwarp();
             }
-            // also after an abort: the teardown waits for it
-            if constexpr (FORM == PAIR) umma2_commit_elect(acc_full(b));
-            else umma_commit_elect(acc_full(b));
+            // after an abort the teardown waits for it
+            if (!ok && elect_one()) commit(acc_full(b));
+            __syncwarp();
         }
         // every MMA issued has completed before the tensor memory is given up
         if (!ok)
