@@ -173,7 +173,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     using C = G8Cfg<FORM>;
     constexpr int EPI_WARPS = C::EPI_WARPS, TMA_WARP = C::TMA_WARP, MMA_WARP = C::MMA_WARP, CW = C::CW;
     extern __shared__ __align__(1024) unsigned char dsm[];
-    __shared__ __align__(8) uint64_t bars[3 * MAX_STAGES + 4 + 2 * SLOTS];
+    __shared__ __align__(8) uint64_t bars[2 * MAX_STAGES + 4 + 2 * SLOTS];
     __shared__ float staged[SLOTS][SLOT_FLOATS];
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t abort_word;
@@ -190,20 +190,19 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     const uint32_t bar0 = smem_addr(bars);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
-    auto peer_full = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + s); };      // PAIR, even CTA
-    auto acc_full = [&](int b) { return bar0 + 8u * (3 * MAX_STAGES + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (3 * MAX_STAGES + 2 + b); };
-    auto sc_full = [&](int n) { return bar0 + 8u * (3 * MAX_STAGES + 4 + n); };
-    auto sc_empty = [&](int n) { return bar0 + 8u * (3 * MAX_STAGES + 4 + SLOTS + n); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + 2 + b); };
+    auto sc_full = [&](int n) { return bar0 + 8u * (2 * MAX_STAGES + 4 + n); };
+    auto sc_empty = [&](int n) { return bar0 + 8u * (2 * MAX_STAGES + 4 + SLOTS + n); };
 
+    const uint32_t rank = FORM == ONE ? 0u : cluster_rank(), size = FORM == ONE ? 1u : cluster_size();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* err = a.err ? a.err : &unrecorded;
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;      // flags are raised only by waits that ran out
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(full_bar(s), 1);
+            mbar_init(full_bar(s), FORM == PAIR && rank == 0 ? 2 : 1);      // in a pair's even CTA, the other's word, too
             mbar_init(empty_bar(s), 1);
-            mbar_init(peer_full(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
@@ -226,7 +225,6 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     fence_after();
     const uint32_t tmem = tmem_slot;
 
-    const uint32_t rank = FORM == ONE ? 0u : cluster_rank(), size = FORM == ONE ? 1u : cluster_size();
     const int g_lo = FORM == SPLIT ? static_cast<int>(static_cast<int64_t>(a.G) * rank / size) : 0;
     const int g_hi = FORM == SPLIT ? static_cast<int>(static_cast<int64_t>(a.G) * (rank + 1) / size) : a.G;
     const int units = a.m_tiles * a.n_tiles;
@@ -337,7 +335,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_remote(peer_full(s), 0);
+                if (lane == 0) mbar_arrive_remote(full_bar(s), 0);
                 __syncwarp();
                 if (++s == stages) {
                     s = 0;
@@ -347,6 +345,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
         }
     } else if (warp == MMA_WARP) {
         const uint32_t idesc = idesc_e4m3(FORM == PAIR ? 2 * TM : TM, a.bn);
+        const uint64_t ad0 = smem_desc(a_tile(0)), bd0 = smem_desc(b_tile(0));
         int it = 0, s = 0;
         uint32_t ph = 0u;
         bool ok = true;
@@ -354,14 +353,13 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
             for (int g = g_lo; g < g_hi; ++g, ++it) {
                 const int b = it & 1;
                 if (!__all_sync(FULL_MASK, mbar_wait(full_bar(s), ph, abort_flag, err, 2u) &&
-                                               (FORM != PAIR || mbar_wait(peer_full(s), ph, abort_flag, err, 2u)) &&
                                                mbar_wait(acc_empty(b), (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, abort_flag,
                                                          err, 2u))) {
                     ok = false;
                     break;
                 }
                 fence_after();
-                const uint64_t ad = smem_desc(a_tile(s)), bd = smem_desc(b_tile(s));
+                const uint64_t ad = ad0 + static_cast<uint32_t>(s) * (a_bytes >> 4), bd = bd0 + static_cast<uint32_t>(s) * (C::B_BYTES >> 4);
                 const uint32_t d = tmem + static_cast<uint32_t>(b * C::BUF);
                 if (elect_one()) {
 #pragma unroll

@@ -13,13 +13,17 @@
 // K-major for dgrad (a row of dY runs along r = i), N-major for wgrad (it
 // runs along n = m).
 //
-// Three rings, each with its own full and empty barriers: C, the compressed
-// operand as it lies in HBM (TMA; 64 rows of 128 codes, or of 4 plane words
-// per path); A, its expansion; B, the dY tiles. The expansion only waits for
-// C and for a free slot of A, so neither load's latency meets it.
+// Two rings: C, the compressed operand as it lies in HBM (TMA; 64 rows of 128
+// codes, or of 4 plane words per path) with its rows' scales, and the stages, its expansion A beside
+// the dY tile B (TMA). A stage has one full barrier, for the expansion's
+// arrivals and B's bytes, and one empty barrier: the MMA warp issues a stage's
+// MMAs in about 300 cycles when it waits once and commits once, and took
+// 550 with separate barriers for A and B, more than the 512 that the MMAs
+// of a 256-wide tile last.
 //
 // Roles: warps 0-3 epilogue, then two or three groups of four expansion warps
-// that take the stages in turn, and one warp each for B loads, MMAs and C loads.
+// that take the stages in turn, and one warp each for B loads, MMAs, C loads
+// (WARP) scales.
 // Three forms:
 //   ONE    a CTA walks its 128 x BN tiles with two accumulators, so the
 //          epilogue of a tile overlaps the next tile's MMAs;
@@ -55,26 +59,37 @@ constexpr uint32_t A_BYTES = 128 * BR * 2;      // two chunks of [64 r][64 j]
 constexpr uint32_t CHUNK = 64 * BR * 2;         // 8 KB
 enum : int { DGRAD = 0, WGRAD = 1 };
 enum : int { ONE = 0, SPLIT = 1, PAIR = 2 };
+// How a stage's scales (of all paths) reach shared memory:
+//   ROWS   one scale per row: a TMA box of 64 consecutive values of each path;
+//   BOX    one per row and 128 columns: a TMA box of 64 rows x 16 bytes of
+//          each path, the tile's column among them;
+//   WARP   where TMA cannot address them (a path's or a row's scales not a
+//          multiple of 16 bytes): one warp loads and stores them, 4 stages ahead.
+// One TMA for the scales and one for the plane words of all paths: the issuing
+// thread needs about 200 cycles for each, and four or more a stage took
+// longer than everything else in it.
+enum : int { ROWS = 0, BOX = 1, WARP = 2 };
 
 template <int MODE, int NP, int BN, int FORM>
 struct BwCfg {
     static constexpr int BNC = FORM == PAIR ? BN / 2 : BN;      // rows of the dY tile in this CTA
     static constexpr uint32_t B_BYTES = BNC * BR * 2;
     static constexpr uint32_t C_BYTES = MODE == WGRAD ? 128 * BR : NP * 16 * BR;
+    static constexpr uint32_t S_BYTES = NP * 16 * BR;      // most bytes of a stage's scales
     // expansion groups: a stage's MMAs take 2 BN cycles, a group's stage about 1000
     static constexpr int GROUPS = 3;
-    static constexpr int B_WARP = EXP_WARP0 + GROUPS * GROUP_WARPS, MMA_WARP = B_WARP + 1, C_WARP = B_WARP + 2;
-    static constexpr int THREADS = 32 * (C_WARP + 1);
-    static constexpr int AS = BNC >= 256 ? 3 : 4, BS = BNC >= 256 ? 4 : 6, CS = MODE == WGRAD ? 5 : 6;
-    static constexpr uint32_t TILES = AS * A_BYTES + BS * B_BYTES + CS * C_BYTES;
-    static constexpr int BARS = 2 * (AS + BS + CS) + 4 + AS;
+    static constexpr int B_WARP = EXP_WARP0 + GROUPS * GROUP_WARPS, MMA_WARP = B_WARP + 1, C_WARP = B_WARP + 2, S_WARP = B_WARP + 3;
+    static constexpr int THREADS = 32 * (S_WARP + 1);
+    static constexpr int ST = MODE == WGRAD || NP > 2 ? 5 : 6, CS = ST;
+    static constexpr uint32_t STAGE = A_BYTES + B_BYTES, TILES = ST * STAGE + CS * (C_BYTES + S_BYTES);
+    static constexpr int BARS = 2 * (ST + CS) + 4;
     // at least 120 KB, so that two CTAs never share an SM's tensor memory
     static constexpr uint32_t SMEM = (TILES < 119u * 1024u ? 119u * 1024u : TILES) + 1024u;
     static constexpr uint32_t TMEM_COLS = 2 * BN;
     static_assert(SMEM + 512 <= 227 * 1024, "shared memory");
-    static_assert(BN * 512u <= TILES || BN <= 128, "a split tile's sums do not fit the rings");
+    static_assert(FORM != SPLIT || BN * 512u <= TILES, "a split tile's sums do not fit the rings");
     // the groups wait on slots that their own previous stage has passed
-    static_assert(GROUPS <= AS && GROUPS <= CS, "a group could run two phases ahead of a slot");
+    static_assert(GROUPS <= ST && GROUPS <= CS, "a group could run two phases ahead of a slot");
 };
 
 struct BwArgs {
@@ -89,6 +104,10 @@ struct BwArgs {
     int j_tiles, n_tiles;
     int out_dt;
     bool sliced, alpha_f16, g128;
+    int scales_by;
+    bool scales_f16;            // as they lie in shared memory
+    uint32_t scale_row, scale_path;     // bytes from one row's and from one path's to the next there
+    uint32_t scale_bytes;       // of a stage's TMA box
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -136,9 +155,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
-// Walks the scales of a thread's two rows per stage, UROWS apart, stage after
-// stage of its group (0 past the last row, so that the row adds nothing).
-template <int MODE, int NP, int UROWS, int STEP>
+// Walks the scales of a lane's two rows of a stage (lane and lane + 32), stage
+// after stage (0 past the last row, so that the row adds nothing).
+template <int MODE, int NP>
 struct ScaleWalk {
     const char* at;
     int64_t path, row;       // bytes between paths and between rows
@@ -156,27 +175,29 @@ struct ScaleWalk {
     __device__ __forceinline__ void load(float (&v)[2][NP]) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const bool in = left > k * UROWS;
+            const bool in = left > k * 32;
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                const char* q = at + k * UROWS * row + p * path;
+                const char* q = at + k * 32 * row + p * path;
                 v[k][p] = 0.0f;
                 if (in) v[k][p] = f16 ? __half2float(__ldg(reinterpret_cast<const __half*>(q))) : __ldg(reinterpret_cast<const float*>(q));
             }
         }
-        at += STEP * row;
-        left -= STEP;
+        at += BR * row;
+        left -= BR;
     }
 };
 
-// 32 weights sum_p +-al_p from the 32 bits of w[p]: path 0 gives the sign, the
-// paths that agree or disagree with it choose one of 2^(NP-1) magnitudes.
+// 32 weights from the 32 bits of w[p]: path 0 gives the sign, the paths that
+// agree or disagree with it choose one of 2^(NP-1) magnitudes.
 // h[i] holds columns i and i + 16 of the word: a left shift by 15 - i puts both
 // sign bits in place, and a byte's top bit spread over 16 bits by PRMT gives
 // both choices at once. The columns of a tile are thus permuted within 32
 // (position 2i: column i, 2i + 1: column i + 16), which the epilogue undoes.
 template <int NP, bool BF16>
 __device__ __forceinline__ void expand_planes(const uint32_t (&w)[NP], const float (&al)[NP], uint32_t (&h)[16]) {
+    // of bit p - 1 of m: path p agrees with path 0 (the sum of up to four
+    // scales is rounded to fp32, then once to dY's type)
     constexpr int NM = 1 << (NP - 1);
     uint32_t mag[NM];
 #pragma unroll
@@ -244,6 +265,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ float lds_scale(uint32_t addr, bool f16) {
+    if (f16) {
+        uint16_t h;
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(addr) : "memory");
+        return __half2float(__ushort_as_half(h));
+    }
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -305,45 +336,41 @@ __device__ __forceinline__ void store_rows(void* out, const void* add, int64_t a
 
 template <int MODE, int NP, int BN, bool BF16, int FORM>
 __global__ void __launch_bounds__(BwCfg<MODE, NP, BN, FORM>::THREADS, 1)
-gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap cmap, BwArgs a) {
+gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap cmap,
+                const __grid_constant__ CUtensorMap smap, BwArgs a) {
     using C = BwCfg<MODE, NP, BN, FORM>;
-    constexpr int AS = C::AS, BS = C::BS, CS = C::CS, GROUPS = C::GROUPS;
-    constexpr int B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP;
+    constexpr int ST = C::ST, CS = C::CS, GROUPS = C::GROUPS;
+    constexpr int B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP, S_WARP = C::S_WARP;
     extern __shared__ __align__(1024) unsigned char dsm[];
     __shared__ __align__(8) uint64_t bars[C::BARS];
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t abort_word;
     volatile uint32_t* abort_flag = &abort_word;
     const uint32_t tiles = (smem_addr(dsm) + 1023u) & ~1023u;
-    auto a_tile = [&](int s) { return tiles + static_cast<uint32_t>(s) * A_BYTES; };
-    auto b_tile = [&](int s) { return tiles + AS * A_BYTES + static_cast<uint32_t>(s) * C::B_BYTES; };
-    auto c_tile = [&](int s) { return tiles + AS * A_BYTES + BS * C::B_BYTES + static_cast<uint32_t>(s) * C::C_BYTES; };
+    auto a_tile = [&](int s) { return tiles + static_cast<uint32_t>(s) * C::STAGE; };
+    auto b_tile = [&](int s) { return a_tile(s) + A_BYTES; };
+    auto c_tile = [&](int s) { return tiles + ST * C::STAGE + static_cast<uint32_t>(s) * C::C_BYTES; };
+    auto s_tile = [&](int s) { return tiles + ST * C::STAGE + CS * C::C_BYTES + static_cast<uint32_t>(s) * C::S_BYTES; };
     const uint32_t bar0 = smem_addr(bars);
-    auto full_a = [&](int s) { return bar0 + 8u * s; };
-    auto empty_a = [&](int s) { return bar0 + 8u * (AS + s); };
-    auto full_b = [&](int s) { return bar0 + 8u * (2 * AS + s); };
-    auto empty_b = [&](int s) { return bar0 + 8u * (2 * AS + BS + s); };
-    auto full_c = [&](int s) { return bar0 + 8u * (2 * AS + 2 * BS + s); };
-    auto empty_c = [&](int s) { return bar0 + 8u * (2 * AS + 2 * BS + CS + s); };
-    auto acc_full = [&](int b) { return bar0 + 8u * (2 * (AS + BS + CS) + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * (AS + BS + CS) + 2 + b); };
-    auto peer_full = [&](int s) { return bar0 + 8u * (2 * (AS + BS + CS) + 4 + s); };      // PAIR, even CTA
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (ST + s); };
+    auto full_c = [&](int s) { return bar0 + 8u * (2 * ST + s); };
+    auto empty_c = [&](int s) { return bar0 + 8u * (2 * ST + CS + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (2 * (ST + CS) + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * (ST + CS) + 2 + b); };
 
+    const uint32_t rank = FORM == ONE ? 0u : cluster_rank(), size = FORM == ONE ? 1u : cluster_size();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* err = a.err ? a.err : &unrecorded;
     if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;      // flags are raised only by waits that ran out
     if (threadIdx.x == 0) {
-        for (int s = 0; s < AS; ++s) {
-            mbar_init(full_a(s), GROUP_WARPS);
-            mbar_init(empty_a(s), 1);
-            mbar_init(peer_full(s), 1);
-        }
-        for (int s = 0; s < BS; ++s) {
-            mbar_init(full_b(s), 1);
-            mbar_init(empty_b(s), 1);
+        for (int s = 0; s < ST; ++s) {
+            // four expansion warps, the B loads, and in a pair's even CTA the other's word
+            mbar_init(full_bar(s), GROUP_WARPS + 1 + (FORM == PAIR && rank == 0 ? 1 : 0));
+            mbar_init(empty_bar(s), 1);
         }
         for (int s = 0; s < CS; ++s) {
-            mbar_init(full_c(s), 1);
+            mbar_init(full_c(s), a.scales_by == WARP ? 2 : 1);
             mbar_init(empty_c(s), GROUP_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
@@ -363,7 +390,6 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     fence_after();
     const uint32_t tmem = tmem_slot;
 
-    const uint32_t rank = FORM == ONE ? 0u : cluster_rank(), size = FORM == ONE ? 1u : cluster_size();
     const int64_t nr = (a.R + BR - 1) / BR;
     const int r_lo = FORM == SPLIT ? static_cast<int>(nr * rank / size) : 0;
     const int r_hi = FORM == SPLIT ? static_cast<int>(nr * (rank + 1) / size) : static_cast<int>(nr);
@@ -378,119 +404,142 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
 
     if (warp == B_WARP) {
         if (lane == 0) {
-            Ring<BS> q;
+            Ring<ST> q;
             int it = 0;
             bool ok = true;
             for (int u = u0; u < units && ok; u += u_step) {
                 const int n0 = n_tile(u) * BN + (FORM == PAIR ? static_cast<int>(rank) * C::BNC : 0);
                 for (int rb = r_lo; rb < r_hi; ++rb, ++it, q.next()) {
-                    if (!mbar_wait(empty_b(q.slot), q.ph ^ 1u, abort_flag, err, 1u)) {
+                    if (!mbar_wait(empty_bar(q.slot), q.ph ^ 1u, abort_flag, err, 1u)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(full_b(q.slot), C::B_BYTES);
+                    mbar_arrive_expect_tx(full_bar(q.slot), C::B_BYTES);
                     if constexpr (MODE == DGRAD) {
-                        tma_load_2d(b_tile(q.slot), &dmap, rb * BR, n0, full_b(q.slot));
+                        tma_load_2d(b_tile(q.slot), &dmap, rb * BR, n0, full_bar(q.slot));
                     } else {
 #pragma unroll
                         for (int c = 0; c < C::BNC / 64; ++c)
-                            tma_load_2d(b_tile(q.slot) + c * CHUNK, &dmap, n0 + c * 64, rb * BR, full_b(q.slot));
+                            tma_load_2d(b_tile(q.slot) + c * CHUNK, &dmap, n0 + c * 64, rb * BR, full_bar(q.slot));
                     }
                 }
             }
             // after an abort the loads in flight land before the CTA gives up its shared memory
+            // (the expansion may have left: the barrier's phase may stay open)
             if (*abort_flag)
-                for (int i = it - 1; i >= 0 && i >= it - BS; --i)
-                    mbar_drain(full_b(i % BS), static_cast<uint32_t>(i / BS) & 1u);
+                for (int i = it - 1; i >= 0 && i >= it - ST; --i)
+                    mbar_drain(full_bar(i % ST), static_cast<uint32_t>(i / ST) & 1u);
             // the even CTA's commits also arrive here: all of them, before the CTA may go
             else if (FORM == PAIR)
-                for (int i = it - 1; i >= 0 && i >= it - BS; --i)
-                    mbar_drain(empty_b(i % BS), static_cast<uint32_t>(i / BS) & 1u);
+                for (int i = it - 1; i >= 0 && i >= it - ST; --i)
+                    mbar_drain(empty_bar(i % ST), static_cast<uint32_t>(i / ST) & 1u);
         }
     } else if (warp == C_WARP) {
         if (lane == 0) {
             Ring<CS> q;
             int it = 0;
             bool ok = true;
-            const int S = static_cast<int>((a.J + 511) >> 9);
             for (int u = u0; u < units && ok; u += u_step) {
                 const int jt = j_tile(u);
+                const int x = a.sliced ? (jt & 3) * 4 : jt * 4, z = a.sliced ? jt >> 2 : 0;      // plane words of the tile
+                const int xs = a.scales_f16 ? jt & ~7 : jt & ~3;
                 for (int rb = r_lo; rb < r_hi; ++rb, ++it, q.next()) {
                     if (!mbar_wait(empty_c(q.slot), q.ph ^ 1u, abort_flag, err, 1u)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(full_c(q.slot), C::C_BYTES);
-                    if constexpr (MODE == WGRAD) {
-                        tma_load_3d(c_tile(q.slot), &cmap, jt * 128, rb * BR, 0, full_c(q.slot));
-                    } else {
-#pragma unroll
-                        for (int p = 0; p < NP; ++p) {
-                            const int x = a.sliced ? (jt & 3) * 4 : jt * 4, z = a.sliced ? p * S + (jt >> 2) : p;
-                            tma_load_3d(c_tile(q.slot) + p * 16 * BR, &cmap, x, rb * BR, z, full_c(q.slot));
-                        }
-                    }
+                    mbar_arrive_expect_tx(full_c(q.slot), C::C_BYTES + a.scale_bytes);
+                    if constexpr (MODE == WGRAD) tma_load_3d(c_tile(q.slot), &cmap, jt * 128, rb * BR, 0, full_c(q.slot));
+                    else tma_load_4d(c_tile(q.slot), &cmap, x, rb * BR, z, 0, full_c(q.slot));
+                    if (a.scales_by == ROWS) tma_load_3d(s_tile(q.slot), &smap, rb * BR, 0, 0, full_c(q.slot));
+                    else if (a.scales_by == BOX) tma_load_3d(s_tile(q.slot), &smap, xs, rb * BR, 0, full_c(q.slot));
                 }
             }
+            // (the scale warp may have left: the barrier's phase may stay open)
             if (*abort_flag)
                 for (int i = it - 1; i >= 0 && i >= it - CS; --i)
                     mbar_drain(full_c(i % CS), static_cast<uint32_t>(i / CS) & 1u);
         }
+    } else if (warp == S_WARP) {
+        constexpr int PD = 4;                     // stages read ahead
+        Ring<CS> q;
+        bool ok = a.scales_by == WARP;
+        for (int u = u0; u < units && ok; u += u_step) {
+            ScaleWalk<MODE, NP> walk;
+            walk.start(a, static_cast<int64_t>(r_lo) * BR + lane, j_tile(u));
+            float v[PD][2][NP];
+#pragma unroll
+            for (int i = 0; i < PD; ++i) walk.load(v[i]);
+            for (int rb0 = r_lo; rb0 < r_hi && ok; rb0 += PD) {
+#pragma unroll
+                for (int i = 0; i < PD; ++i) {
+                    if (rb0 + i < r_hi && ok) {
+                        ok = __all_sync(FULL_MASK, mbar_wait(empty_c(q.slot), q.ph ^ 1u, abort_flag, err, 1u));
+                        if (ok) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int p = 0; p < NP; ++p)
+                                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_tile(q.slot) + p * a.scale_path + (lane + 32 * k) * 4u),
+                                                 "f"(v[i][k][p])
+                                                 : "memory");
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(full_c(q.slot));
+                            walk.load(v[i]);
+                            q.next();
+                        }
+                    }
+                }
+            }
+        }
     } else if (FORM == PAIR && warp == MMA_WARP && rank == 1) {
         // the pair's MMAs are issued by the even CTA: tell it, stage by stage,
         // that this CTA's half of the operands is there
-        Ring<AS> qa;
-        Ring<BS> qb;
+        Ring<ST> q;
         bool ok = true;
-        int it = 0;
         for (int u = u0; u < units && ok; u += u_step) {
-            for (int rb = r_lo; rb < r_hi; ++rb, ++it, qa.next(), qb.next()) {
-                if (!__all_sync(FULL_MASK, mbar_wait(full_b(qb.slot), qb.ph, abort_flag, err, 2u) &&
-                                               mbar_wait(full_a(qa.slot), qa.ph, abort_flag, err, 2u))) {
+            for (int rb = r_lo; rb < r_hi; ++rb, q.next()) {
+                if (!__all_sync(FULL_MASK, mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u))) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_remote(peer_full(qa.slot), 0);
+                if (lane == 0) mbar_arrive_remote(full_bar(q.slot), 0);
                 __syncwarp();
             }
         }
-        if (ok)
-            for (int i = it - 1; i >= 0 && i >= it - AS; --i) mbar_drain(empty_a(i % AS), static_cast<uint32_t>(i / AS) & 1u);
     } else if (warp == MMA_WARP) {
         constexpr uint32_t idesc = idesc_bw(BN, BF16, MODE == WGRAD, FORM == PAIR ? 256 : BM);
         auto commit = [](uint32_t bar) {
             if constexpr (FORM == PAIR) umma2_commit(bar);
             else umma_commit(bar);
         };
-        Ring<AS> qa;
-        Ring<BS> qb;
+        Ring<ST> q;
         int tile = 0;
         bool ok = true;
+        // the low words of the descriptors of slot 0 (the high words do not change)
+        const uint64_t ad0 = smem_desc_mn(a_tile(0)), bd0 = MODE == DGRAD ? smem_desc(b_tile(0)) : smem_desc_mn(b_tile(0));
+        // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
+        constexpr uint32_t A_STEP = 128u, B_STEP = MODE == DGRAD ? 2u : 128u;
         for (int u = u0; u < units && ok; u += u_step, ++tile) {
             const int b = tile & 1;
-            const uint32_t aph = (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u;
+            const uint32_t aph = (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u, d = tmem + static_cast<uint32_t>(b * BN);
             ok = __all_sync(FULL_MASK, mbar_wait(acc_empty(b), aph, abort_flag, err, 2u));
-            for (int rb = r_lo; rb < r_hi && ok; ++rb, qa.next(), qb.next()) {
-                if (!__all_sync(FULL_MASK, mbar_wait(full_b(qb.slot), qb.ph, abort_flag, err, 2u) &&
-                                               mbar_wait(full_a(qa.slot), qa.ph, abort_flag, err, 2u) &&
-                                               (FORM != PAIR || mbar_wait(peer_full(qa.slot), qa.ph, abort_flag, err, 2u)))) {
+            for (int rb = r_lo; rb < r_hi && ok; ++rb, q.next()) {
+                if (!__all_sync(FULL_MASK, mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u))) {
                     ok = false;
                     break;
                 }
                 fence_after();
+                const uint32_t off = static_cast<uint32_t>(q.slot) * (C::STAGE >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < BR / 16; ++kk) {
-                        // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
-                        const uint64_t ad = smem_desc_mn(a_tile(qa.slot)) + 128u * kk;
-                        const uint64_t bd = MODE == DGRAD ? smem_desc(b_tile(qb.slot)) + 2u * kk
-                                                          : smem_desc_mn(b_tile(qb.slot)) + 128u * kk;
-                        const uint32_t d = tmem + static_cast<uint32_t>(b * BN), more = (rb > r_lo || kk > 0) ? 1u : 0u;
+                        const uint64_t ad = ad0 + off + A_STEP * kk, bd = bd0 + off + B_STEP * kk;
+                        const uint32_t more = (rb > r_lo || kk > 0) ? 1u : 0u;
                         if constexpr (FORM == PAIR) umma2_f16(d, ad, bd, idesc, more);
                         else umma_f16(d, ad, bd, idesc, more);
                     }
-                    commit(empty_a(qa.slot));
-                    commit(empty_b(qb.slot));
+                    commit(empty_bar(q.slot));
                     if (rb + 1 == r_hi) commit(acc_full(b));
                 }
                 __syncwarp();
@@ -519,7 +568,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         const uint32_t c0 = static_cast<uint32_t>(wd & 1) * 4u;
         const uint32_t cx = MODE == DGRAD && wd >= 2 ? 2u : 0u;
         const uint32_t bytes = cx ? 0x2301u : 0x3210u;
-        Ring<AS> qa;
+        Ring<ST> qa;
         Ring<CS> qc;
         bool ok = true;
         int it = 0;                      // stages before this tile, modulo GROUPS
@@ -527,13 +576,9 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         qc.next(grp);
         for (int u = u0; u < units && ok; u += u_step, it = (it + r_hi - r_lo) % GROUPS) {
             int rb = r_lo + (grp - it + GROUPS) % GROUPS;          // the group's first stage of this tile
-            ScaleWalk<MODE, NP, UROWS, GROUPS * BR> walk;
-            walk.start(a, static_cast<int64_t>(rb) * BR + row, j_tile(u));
-            float cur[2][NP], nxt[2][NP], far[2][NP];
-            walk.load(cur);
-            walk.load(nxt);
+            // the tile's column among the 16 bytes of a row's scales
+            const uint32_t scale_at = a.scales_by != BOX ? 0u : a.scales_f16 ? (j_tile(u) & 7) * 2u : (j_tile(u) & 3) * 4u;
             for (; rb < r_hi; rb += GROUPS, qa.next(GROUPS), qc.next(GROUPS)) {
-                walk.load(far);
                 if (!__all_sync(FULL_MASK, mbar_wait(full_c(qc.slot), qc.ph, abort_flag, err, 4u))) {
                     ok = false;
                     break;
@@ -542,22 +587,26 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t r = row + k * UROWS;
+                    float sc[NP];
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        sc[p] = lds_scale(s_tile(qc.slot) + p * a.scale_path + r * a.scale_row + scale_at, a.scales_f16);
                     if constexpr (MODE == WGRAD) {
                         const uint32_t base = c_tile(qc.slot) + r * 128u;
                         const uint4 x = lds128(base + (((2u * wd) ^ sw) << 4)), y = lds128(base + (((2u * wd + 1u) ^ sw) << 4));
                         const uint32_t c[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                        expand_codes<BF16>(c, cur[k][0], h[k]);
+                        expand_codes<BF16>(c, sc[0], h[k]);
                     } else {
                         uint32_t w[NP];
 #pragma unroll
                         for (int p = 0; p < NP; ++p)
                             w[p] = prmt(lds32(c_tile(qc.slot) + p * 16u * BR + r * 16u + 4u * wd), 0u, bytes);
-                        expand_planes<NP, BF16>(w, cur[k], h[k]);
+                        expand_planes<NP, BF16>(w, sc, h[k]);
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_c(qc.slot));
-                if (!__all_sync(FULL_MASK, mbar_wait(empty_a(qa.slot), qa.ph ^ 1u, abort_flag, err, 4u))) {
+                if (!__all_sync(FULL_MASK, mbar_wait(empty_bar(qa.slot), qa.ph ^ 1u, abort_flag, err, 4u))) {
                     ok = false;
                     break;
                 }
@@ -570,14 +619,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 }
                 fence_proxy_async_smem();   // make the generic-proxy stores visible to the tensor core
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full_a(qa.slot));
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        cur[k][p] = nxt[k][p];
-                        nxt[k][p] = far[k][p];
-                    }
+                if (lane == 0) mbar_arrive(full_bar(qa.slot));
             }
         }
     } else {
@@ -648,18 +690,54 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     }
 }
 
-// Plane words in boxes of 4 words (one 128-column tile) x 64 rows of one path:
-// [N][M][K/32], or [N * S][M][16] in the sliced order.
+struct BwMaps {
+    CUtensorMap dy, c, s;
+};
+
+// How the scales [n][R] or [n][R][J / 128] come to shared memory, and their map.
+cudaError_t plan_scales(CUtensorMap* map, BwArgs& a, const void* scales, int n) {
+    const bool per_block = a.g128 || a.codes;
+    const cuuint32_t es = a.alpha_f16 ? 2 : 4;
+    const cuuint64_t inner = static_cast<cuuint64_t>(per_block ? a.J / 128 : a.R);
+    if (reinterpret_cast<uintptr_t>(scales) % 16 != 0 || inner * es % 16 != 0) {
+        a.scales_by = WARP;
+        a.scales_f16 = false;
+        a.scale_row = 4;
+        a.scale_path = 4 * BR;
+        a.scale_bytes = 0;
+        return cudaSuccess;
+    }
+    a.scales_by = per_block ? BOX : ROWS;
+    a.scales_f16 = a.alpha_f16;
+    a.scale_row = per_block ? 16 : es;
+    a.scale_path = a.scale_row * BR;
+    a.scale_bytes = a.scale_path * n;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {inner, static_cast<cuuint64_t>(per_block ? a.R : n), static_cast<cuuint64_t>(per_block ? n : 1)};
+    const cuuint64_t strides[2] = {inner * es, inner * es * dims[1]};
+    const cuuint32_t box[3] = {per_block ? 16 / es : BR, static_cast<cuuint32_t>(per_block ? BR : n),
+                               static_cast<cuuint32_t>(per_block ? n : 1)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(scales), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+
+// Plane words in boxes of 4 words (one 128-column tile) x 64 rows of every
+// path: [N][1][M][K/32], or [N][S][M][16] in the sliced order.
 cudaError_t make_planes_map(CUtensorMap* map, const BwArgs& a, int n_paths) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
     const cuuint64_t words = a.sliced ? 16 : static_cast<cuuint64_t>(a.J / 32);
-    const cuuint64_t dims[3] = {words, static_cast<cuuint64_t>(a.R),
-                                static_cast<cuuint64_t>(n_paths) * (a.sliced ? (a.J + 511) / 512 : 1)};
-    const cuuint64_t strides[2] = {words * 4, words * 4 * a.R};
-    const cuuint32_t box[3] = {4u, static_cast<cuuint32_t>(BR), 1u};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint32_t*>(a.planes), dims, strides, box, estr,
+    const cuuint64_t slices = a.sliced ? static_cast<cuuint64_t>((a.J + 511) / 512) : 1;
+    const cuuint64_t dims[4] = {words, static_cast<cuuint64_t>(a.R), slices, static_cast<cuuint64_t>(n_paths)};
+    const cuuint64_t strides[3] = {words * 4, words * 4 * a.R, words * 4 * a.R * slices};
+    const cuuint32_t box[4] = {4u, static_cast<cuuint32_t>(BR), 1u, static_cast<cuuint32_t>(n_paths)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<uint32_t*>(a.planes), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
@@ -667,7 +745,7 @@ cudaError_t make_planes_map(CUtensorMap* map, const BwArgs& a, int n_paths) {
 }
 
 template <int MODE, int NP, int BN, bool BF16, int FORM>
-cudaError_t launch(const CUtensorMap& m, const CUtensorMap& c, BwArgs& a, int cluster, cudaStream_t s) {
+cudaError_t launch(const BwMaps& m, BwArgs& a, int cluster, cudaStream_t s) {
     constexpr size_t smem = BwCfg<MODE, NP, BN, FORM>::SMEM;
     auto kern = gemm_bwd_kernel<MODE, NP, BN, BF16, FORM>;
     static SmemMark mark;
@@ -687,18 +765,18 @@ cudaError_t launch(const CUtensorMap& m, const CUtensorMap& c, BwArgs& a, int cl
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = FORM == ONE ? 0 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, m, c, a);
+    return cudaLaunchKernelEx(&cfg, kern, m.dy, m.c, m.s, a);
 }
 
 template <int MODE, int NP, int BN>
-cudaError_t launch_bn(const CUtensorMap& m, const CUtensorMap& c, BwArgs& a, bool bf16, cudaStream_t s) {
+cudaError_t launch_bn(const BwMaps& m, BwArgs& a, bool bf16, cudaStream_t s) {
     a.n_tiles = static_cast<int>((a.N + BN - 1) / BN);
     const int64_t units = static_cast<int64_t>(a.j_tiles) * a.n_tiles, nr = (a.R + BR - 1) / BR;
     int split = 1;
     while (split < 8 && units * (split + 1) <= device_sm_count() && split < nr) ++split;
     if (split > 1)
-        return bf16 ? launch<MODE, NP, BN, true, SPLIT>(m, c, a, split, s) : launch<MODE, NP, BN, false, SPLIT>(m, c, a, split, s);
-    return bf16 ? launch<MODE, NP, BN, true, ONE>(m, c, a, 1, s) : launch<MODE, NP, BN, false, ONE>(m, c, a, 1, s);
+        return bf16 ? launch<MODE, NP, BN, true, SPLIT>(m, a, split, s) : launch<MODE, NP, BN, false, SPLIT>(m, a, split, s);
+    return bf16 ? launch<MODE, NP, BN, true, ONE>(m, a, 1, s) : launch<MODE, NP, BN, false, ONE>(m, a, 1, s);
 }
 
 // Rows of the dY tile: the narrowest that covers N; 256, as a CTA pair's, where
@@ -712,19 +790,20 @@ int bwd_tile(const BwArgs& a) {
 
 template <int NP>
 cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, cudaStream_t s) {
-    CUtensorMap m, c;
+    BwMaps m;
     const int bn = bwd_tile(a);
-    cudaError_t e = make_x_map(&m, dY, a.R, a.N, ldd, bn == 256 ? 128 : bn);
-    if (e == cudaSuccess) e = make_planes_map(&c, a, NP);
+    cudaError_t e = make_x_map(&m.dy, dY, a.R, a.N, ldd, bn == 256 ? 128 : bn);
+    if (e == cudaSuccess) e = make_planes_map(&m.c, a, NP);
+    if (e == cudaSuccess) e = plan_scales(&m.s, a, a.alpha, NP);
     if (e != cudaSuccess) return e;
     switch (bn) {
-        case 32: return launch_bn<DGRAD, NP, 32>(m, c, a, bf16, s);
-        case 64: return launch_bn<DGRAD, NP, 64>(m, c, a, bf16, s);
-        case 128: return launch_bn<DGRAD, NP, 128>(m, c, a, bf16, s);
+        case 32: return launch_bn<DGRAD, NP, 32>(m, a, bf16, s);
+        case 64: return launch_bn<DGRAD, NP, 64>(m, a, bf16, s);
+        case 128: return launch_bn<DGRAD, NP, 128>(m, a, bf16, s);
         default: break;
     }
     a.n_tiles = static_cast<int>((a.N + 255) / 256);
-    return bf16 ? launch<DGRAD, NP, 256, true, PAIR>(m, c, a, 2, s) : launch<DGRAD, NP, 256, false, PAIR>(m, c, a, 2, s);
+    return bf16 ? launch<DGRAD, NP, 256, true, PAIR>(m, a, 2, s) : launch<DGRAD, NP, 256, false, PAIR>(m, a, 2, s);
 }
 
 }  // namespace
@@ -770,18 +849,19 @@ cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M,
     a.ldo = ldw;
     a.j_tiles = static_cast<int>(K / 128);
     a.out_dt = dw_dt;
-    CUtensorMap m, c;
-    cudaError_t e = make_x_map(&m, dY, M, T, ldd, BR);      // boxes of 64 m x 64 t
-    if (e == cudaSuccess) e = make_x8_map(&c, codes, K, T, 1, BR);
+    BwMaps m;
+    cudaError_t e = make_x_map(&m.dy, dY, M, T, ldd, BR);      // boxes of 64 m x 64 t
+    if (e == cudaSuccess) e = make_x8_map(&m.c, codes, K, T, 1, BR);
+    if (e == cudaSuccess) e = plan_scales(&m.s, a, scales, 1);
     if (e != cudaSuccess) return e;
     switch (bwd_tile(a)) {
         case 32:
-        case 64: return launch_bn<WGRAD, 1, 64>(m, c, a, bf16, s);
-        case 128: return launch_bn<WGRAD, 1, 128>(m, c, a, bf16, s);
+        case 64: return launch_bn<WGRAD, 1, 64>(m, a, bf16, s);
+        case 128: return launch_bn<WGRAD, 1, 128>(m, a, bf16, s);
         default: break;
     }
     a.n_tiles = static_cast<int>((M + 255) / 256);
-    return bf16 ? launch<WGRAD, 1, 256, true, PAIR>(m, c, a, 2, s) : launch<WGRAD, 1, 256, false, PAIR>(m, c, a, 2, s);
+    return bf16 ? launch<WGRAD, 1, 256, true, PAIR>(m, a, 2, s) : launch<WGRAD, 1, 256, false, PAIR>(m, a, 2, s);
 }
 
 }  // namespace rb
