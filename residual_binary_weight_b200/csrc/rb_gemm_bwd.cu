@@ -13,8 +13,8 @@
 // K-major for dgrad (a row of dY runs along r = i), N-major for wgrad (it
 // runs along n = m).
 //
-// Two rings: C, the compressed operand as it lies in HBM (TMA; 64 rows of 128
-// codes, or of 4 plane words per path) with its rows' scales, and the stages, its expansion A beside
+// Two rings: C, the compressed operand as it lies in HBM (64 rows of 128 codes,
+// or of 4 plane words per path) with its rows' scales, and the stages, its expansion A beside
 // the dY tile B (TMA). A stage has one full barrier, for the expansion's
 // arrivals and B's bytes, and one empty barrier: the MMA warp issues a stage's
 // MMAs in about 300 cycles when it waits once and commits once, and took
@@ -22,8 +22,8 @@
 // of a 256-wide tile last.
 //
 // Roles: warps 0-3 epilogue, then two or three groups of four expansion warps
-// that take the stages in turn, and one warp each for B loads, MMAs, C loads
-// (WARP) scales.
+// that take the stages in turn, one warp each for B loads and MMAs, and two for
+// C.
 // Three forms:
 //   ONE    a CTA walks its 128 x BN tiles with two accumulators, so the
 //          epilogue of a tile overlaps the next tile's MMAs;
@@ -60,15 +60,14 @@ constexpr uint32_t CHUNK = 64 * BR * 2;         // 8 KB
 enum : int { DGRAD = 0, WGRAD = 1 };
 enum : int { ONE = 0, SPLIT = 1, PAIR = 2 };
 // How a stage's scales (of all paths) reach shared memory:
-//   ROWS   one scale per row: a TMA box of 64 consecutive values of each path;
-//   BOX    one per row and 128 columns: a TMA box of 64 rows x 16 bytes of
-//          each path, the tile's column among them;
-//   WARP   where TMA cannot address them (a path's or a row's scales not a
-//          multiple of 16 bytes): one warp loads and stores them, 4 stages ahead.
-// One TMA for the scales and one for the plane words of all paths: the issuing
-// thread needs about 200 cycles for each, and four or more a stage took
-// longer than everything else in it.
-enum : int { ROWS = 0, BOX = 1, WARP = 2 };
+//   ASYNC  4-byte asynchronous copies (of fp32 values, or of pairs of fp16
+//          values that hold the wanted ones);
+//   LOADED fp16 scales whose pairs straddle rows or paths: loaded and stored.
+// They, and the 16 bytes of plane words of each row and path, are not fetched
+// by TMA: a box whose rows are 16 bytes takes it about 4 cycles a row, so
+// that the 128 rows of two paths alone took longer (590 cycles a stage) than the
+// MMAs of a 256-wide tile. Two warps copy stages in turn.
+enum : int { ASYNC = 0, LOADED = 1 };
 
 template <int MODE, int NP, int BN, int FORM>
 struct BwCfg {
@@ -78,8 +77,8 @@ struct BwCfg {
     static constexpr uint32_t S_BYTES = NP * 16 * BR;      // most bytes of a stage's scales
     // expansion groups: a stage's MMAs take 2 BN cycles, a group's stage about 1000
     static constexpr int GROUPS = 3;
-    static constexpr int B_WARP = EXP_WARP0 + GROUPS * GROUP_WARPS, MMA_WARP = B_WARP + 1, C_WARP = B_WARP + 2, S_WARP = B_WARP + 3;
-    static constexpr int THREADS = 32 * (S_WARP + 1);
+    static constexpr int B_WARP = EXP_WARP0 + GROUPS * GROUP_WARPS, MMA_WARP = B_WARP + 1, C_WARP = B_WARP + 2, C_WARPS = 2;
+    static constexpr int THREADS = 32 * (C_WARP + C_WARPS);
     static constexpr int ST = MODE == WGRAD || NP > 2 ? 5 : 6, CS = ST;
     static constexpr uint32_t STAGE = A_BYTES + B_BYTES, TILES = ST * STAGE + CS * (C_BYTES + S_BYTES);
     static constexpr int BARS = 2 * (ST + CS) + 4;
@@ -89,7 +88,7 @@ struct BwCfg {
     static_assert(SMEM + 512 <= 227 * 1024, "shared memory");
     static_assert(FORM != SPLIT || BN * 512u <= TILES, "a split tile's sums do not fit the rings");
     // the groups wait on slots that their own previous stage has passed
-    static_assert(GROUPS <= ST && GROUPS <= CS, "a group could run two phases ahead of a slot");
+    static_assert(C_WARPS <= CS && GROUPS <= ST && GROUPS <= CS, "a group could run two phases ahead of a slot");
 };
 
 struct BwArgs {
@@ -107,7 +106,6 @@ struct BwArgs {
     int scales_by;
     bool scales_f16;            // as they lie in shared memory
     uint32_t scale_row, scale_path;     // bytes from one row's and from one path's to the next there
-    uint32_t scale_bytes;       // of a stage's TMA box
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -154,39 +152,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         return *reinterpret_cast<const uint32_t*>(&h);
     }
 }
-
-// Walks the scales of a lane's two rows of a stage (lane and lane + 32), stage
-// after stage (0 past the last row, so that the row adds nothing).
-template <int MODE, int NP>
-struct ScaleWalk {
-    const char* at;
-    int64_t path, row;       // bytes between paths and between rows
-    int64_t left;            // rows from the first of the two to the end
-    bool f16;
-    __device__ __forceinline__ void start(const BwArgs& a, int64_t r, int64_t jt) {
-        const int es = MODE == DGRAD && a.alpha_f16 ? 2 : 4;
-        const bool per_block = MODE == WGRAD || a.g128;
-        row = (per_block ? a.J >> 7 : 1) * es;
-        path = a.R * row;
-        at = static_cast<const char*>(MODE == WGRAD ? static_cast<const void*>(a.scales) : a.alpha) + r * row + (per_block ? jt * es : 0);
-        left = jt < a.j_tiles ? a.R - r : 0;
-        f16 = es == 2;
-    }
-    __device__ __forceinline__ void load(float (&v)[2][NP]) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const bool in = left > k * 32;
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const char* q = at + k * 32 * row + p * path;
-                v[k][p] = 0.0f;
-                if (in) v[k][p] = f16 ? __half2float(__ldg(reinterpret_cast<const __half*>(q))) : __ldg(reinterpret_cast<const float*>(q));
-            }
-        }
-        at += BR * row;
-        left -= BR;
-    }
-};
 
 // 32 weights from the 32 bits of w[p]: path 0 gives the sign, the paths that
 // agree or disagree with it choose one of 2^(NP-1) magnitudes.
@@ -306,6 +271,14 @@ __device__ __forceinline__ void store_out(void* p, int dt, int64_t i, float v) {
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
+// asynchronous copies global -> shared; `in` false: zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+
 __device__ __forceinline__ void to_out(float v, float* p) { *p = v; }
 __device__ __forceinline__ void to_out(float v, __half* p) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void to_out(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
@@ -336,11 +309,11 @@ __device__ __forceinline__ void store_rows(void* out, const void* add, int64_t a
 
 template <int MODE, int NP, int BN, bool BF16, int FORM>
 __global__ void __launch_bounds__(BwCfg<MODE, NP, BN, FORM>::THREADS, 1)
-gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap cmap,
-                const __grid_constant__ CUtensorMap smap, BwArgs a) {
+gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap cmap, BwArgs a) {
     using C = BwCfg<MODE, NP, BN, FORM>;
     constexpr int ST = C::ST, CS = C::CS, GROUPS = C::GROUPS;
-    constexpr int B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP, S_WARP = C::S_WARP;
+    constexpr int B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP;
+    constexpr int C_WARPS = C::C_WARPS;
     extern __shared__ __align__(1024) unsigned char dsm[];
     __shared__ __align__(8) uint64_t bars[C::BARS];
     __shared__ uint32_t tmem_slot;
@@ -370,7 +343,8 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             mbar_init(empty_bar(s), 1);
         }
         for (int s = 0; s < CS; ++s) {
-            mbar_init(full_c(s), a.scales_by == WARP ? 2 : 1);
+            // a copying warp's lanes, and wgrad's codes (TMA)
+            mbar_init(full_c(s), 32 + (MODE == WGRAD ? 1 : 0));
             mbar_init(empty_c(s), GROUP_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
@@ -434,64 +408,93 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 for (int i = it - 1; i >= 0 && i >= it - ST; --i)
                     mbar_drain(empty_bar(i % ST), static_cast<uint32_t>(i / ST) & 1u);
         }
-    } else if (warp == C_WARP) {
-        if (lane == 0) {
-            Ring<CS> q;
-            int it = 0;
-            bool ok = true;
-            for (int u = u0; u < units && ok; u += u_step) {
-                const int jt = j_tile(u);
-                const int x = a.sliced ? (jt & 3) * 4 : jt * 4, z = a.sliced ? jt >> 2 : 0;      // plane words of the tile
-                const int xs = a.scales_f16 ? jt & ~7 : jt & ~3;
-                for (int rb = r_lo; rb < r_hi; ++rb, ++it, q.next()) {
-                    if (!mbar_wait(empty_c(q.slot), q.ph ^ 1u, abort_flag, err, 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(full_c(q.slot), C::C_BYTES + a.scale_bytes);
-                    if constexpr (MODE == WGRAD) tma_load_3d(c_tile(q.slot), &cmap, jt * 128, rb * BR, 0, full_c(q.slot));
-                    else tma_load_4d(c_tile(q.slot), &cmap, x, rb * BR, z, 0, full_c(q.slot));
-                    if (a.scales_by == ROWS) tma_load_3d(s_tile(q.slot), &smap, rb * BR, 0, 0, full_c(q.slot));
-                    else if (a.scales_by == BOX) tma_load_3d(s_tile(q.slot), &smap, xs, rb * BR, 0, full_c(q.slot));
-                }
-            }
-            // (the scale warp may have left: the barrier's phase may stay open)
-            if (*abort_flag)
-                for (int i = it - 1; i >= 0 && i >= it - CS; --i)
-                    mbar_drain(full_c(i % CS), static_cast<uint32_t>(i / CS) & 1u);
-        }
-    } else if (warp == S_WARP) {
-        constexpr int PD = 4;                     // stages read ahead
+    } else if (warp >= C_WARP) {
+        const int mine = warp - C_WARP;
         Ring<CS> q;
-        bool ok = a.scales_by == WARP;
-        for (int u = u0; u < units && ok; u += u_step) {
-            ScaleWalk<MODE, NP> walk;
-            walk.start(a, static_cast<int64_t>(r_lo) * BR + lane, j_tile(u));
-            float v[PD][2][NP];
+        q.next(mine);
+        int issued = 0, it = 0;          // stages of this warp; stages before this tile, modulo C_WARPS
+        bool ok = true;
+        const bool loaded = a.scales_by == LOADED;
+        const bool per_block = MODE == WGRAD || a.g128;
+        // two rows a lane, lane and lane + 32: bytes of a row of words, of a
+        // path of words, of a row and a path of scales
+        const int64_t w_row = a.sliced ? 64 : a.J >> 3, w_path = a.R * w_row * (a.sliced ? (a.J + 511) >> 9 : 1);
+        const int es = MODE == DGRAD && a.alpha_f16 ? 2 : 4;
+        const int64_t s_row = (per_block ? a.J >> 7 : 1) * es, s_path = a.R * s_row;
+        const bool pairs = es == 2 && !per_block && !loaded;          // 32 copies bring 64 rows' fp16 scales
+        const char* planes = reinterpret_cast<const char*>(a.planes);
+        const char* scales = static_cast<const char*>(MODE == WGRAD ? static_cast<const void*>(a.scales) : a.alpha);
+        for (int u = u0; u < units && ok; u += u_step, it = (it + r_hi - r_lo) % C_WARPS) {
+            const int jt = min(j_tile(u), a.j_tiles - 1);
+            int rb = r_lo + (mine - it + C_WARPS) % C_WARPS;
+            int64_t left = a.R - (static_cast<int64_t>(rb) * BR + (pairs ? 2 * lane : lane));     // rows from this lane's first
+            const char* wp = planes + (a.sliced ? static_cast<int64_t>(jt >> 2) * a.R * 64 + (jt & 3) * 16 : static_cast<int64_t>(jt) * 16) +
+                             (static_cast<int64_t>(rb) * BR + lane) * w_row;
+            const char* sp = scales + (per_block ? (static_cast<int64_t>(jt) * es & (loaded ? ~1ll : ~3ll)) : 0) +
+                             (static_cast<int64_t>(rb) * BR + (pairs ? 2 * lane : lane)) * s_row;
+            for (; rb < r_hi; rb += C_WARPS, q.next(C_WARPS), ++issued) {
+                if (!__all_sync(FULL_MASK, mbar_wait(empty_c(q.slot), q.ph ^ 1u, abort_flag, err, 1u))) {
+                    ok = false;
+                    break;
+                }
+                if (MODE == WGRAD && lane == 0) {
+                    mbar_arrive_expect_tx(full_c(q.slot), C::C_BYTES);
+                    tma_load_3d(c_tile(q.slot), &cmap, j_tile(u) * 128, rb * BR, 0, full_c(q.slot));
+                }
+                const int64_t rows_left = pairs ? left + lane : left;      // from row lane of the stage
 #pragma unroll
-            for (int i = 0; i < PD; ++i) walk.load(v[i]);
-            for (int rb0 = r_lo; rb0 < r_hi && ok; rb0 += PD) {
+                for (int k = 0; k < 2; ++k) {
+                    if constexpr (MODE == DGRAD) {
+                        const bool in = rows_left > 32 * k;
+                        const char* src = in ? wp + 32 * k * w_row : planes;
 #pragma unroll
-                for (int i = 0; i < PD; ++i) {
-                    if (rb0 + i < r_hi && ok) {
-                        ok = __all_sync(FULL_MASK, mbar_wait(empty_c(q.slot), q.ph ^ 1u, abort_flag, err, 1u));
-                        if (ok) {
+                        for (int p = 0; p < NP; ++p)
+                            cp_async16(c_tile(q.slot) + p * 16u * BR + (lane + 32 * k) * 16u, src + (in ? p * w_path : 0));
+                    }
+                    if (!pairs && !loaded) {
+                        const bool in = left > 32 * k;
+                        const char* src = in ? sp + 32 * k * s_row : scales;
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                for (int p = 0; p < NP; ++p)
-                                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_tile(q.slot) + p * a.scale_path + (lane + 32 * k) * 4u),
-                                                 "f"(v[i][k][p])
-                                                 : "memory");
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(full_c(q.slot));
-                            walk.load(v[i]);
-                            q.next();
-                        }
+                        for (int p = 0; p < NP; ++p)
+                            cp_async4(s_tile(q.slot) + p * a.scale_path + (lane + 32 * k) * 4u, src + (in ? p * s_path : 0), in);
                     }
                 }
+                if (MODE == DGRAD && pairs) {
+                    const char* src = left > 0 ? sp : scales;               // rows 2 lane and 2 lane + 1
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        cp_async4(s_tile(q.slot) + p * a.scale_path + lane * 4u, src + (left > 0 ? p * s_path : 0), left > 0);
+                }
+                if (MODE == DGRAD && loaded) {
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) {
+                            const float v = left > 32 * k
+                                                ? __half2float(__ldg(reinterpret_cast<const __half*>(sp + 32 * k * s_row + p * s_path)))
+                                                : 0.0f;
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(s_tile(q.slot) + p * a.scale_path + (lane + 32 * k) * 4u), "f"(v)
+                                         : "memory");
+                        }
+                    mbar_arrive(full_c(q.slot));
+                } else {
+                    // arrives once this lane's copies have landed
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full_c(q.slot)) : "memory");
+                }
+                left -= C_WARPS * BR;
+                wp += C_WARPS * BR * w_row;
+                sp += C_WARPS * BR * s_row;
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        // after an abort the codes in flight land before the CTA gives up its shared memory
+        // (the other warp may have left: a barrier's phase may stay open)
+        if (MODE == WGRAD && *abort_flag)
+            for (int i = issued - 1; i >= 0 && i >= issued - CS; --i) {
+                const int n = mine + i * C_WARPS;
+                mbar_drain(full_c(n % CS), static_cast<uint32_t>(n / CS) & 1u);
+            }
     } else if (FORM == PAIR && warp == MMA_WARP && rank == 1) {
         // the pair's MMAs are issued by the even CTA: tell it, stage by stage,
         // that this CTA's half of the operands is there
@@ -576,8 +579,8 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         qc.next(grp);
         for (int u = u0; u < units && ok; u += u_step, it = (it + r_hi - r_lo) % GROUPS) {
             int rb = r_lo + (grp - it + GROUPS) % GROUPS;          // the group's first stage of this tile
-            // the tile's column among the 16 bytes of a row's scales
-            const uint32_t scale_at = a.scales_by != BOX ? 0u : a.scales_f16 ? (j_tile(u) & 7) * 2u : (j_tile(u) & 3) * 4u;
+            // of a pair of fp16 group scales, the tile's
+            const uint32_t scale_at = a.scales_f16 && a.g128 ? (j_tile(u) & 1) * 2u : 0u;
             for (; rb < r_hi; rb += GROUPS, qa.next(GROUPS), qc.next(GROUPS)) {
                 if (!__all_sync(FULL_MASK, mbar_wait(full_c(qc.slot), qc.ph, abort_flag, err, 4u))) {
                     ok = false;
@@ -691,57 +694,19 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
 }
 
 struct BwMaps {
-    CUtensorMap dy, c, s;
+    CUtensorMap dy, c;      // dY, and wgrad's codes
 };
 
-// How the scales [n][R] or [n][R][J / 128] come to shared memory, and their map.
-cudaError_t plan_scales(CUtensorMap* map, BwArgs& a, const void* scales, int n) {
+// How the scales [n][R] or [n][R][J / 128] come to shared memory.
+void plan_scales(BwArgs& a, int n) {
     const bool per_block = a.g128 || a.codes;
-    const cuuint32_t es = a.alpha_f16 ? 2 : 4;
-    const cuuint64_t inner = static_cast<cuuint64_t>(per_block ? a.J / 128 : a.R);
-    if (reinterpret_cast<uintptr_t>(scales) % 16 != 0 || inner * es % 16 != 0) {
-        a.scales_by = WARP;
-        a.scales_f16 = false;
-        a.scale_row = 4;
-        a.scale_path = 4 * BR;
-        a.scale_bytes = 0;
-        return cudaSuccess;
-    }
-    a.scales_by = per_block ? BOX : ROWS;
-    a.scales_f16 = a.alpha_f16;
-    a.scale_row = per_block ? 16 : es;
+    const bool pairs = a.alpha_f16 && !per_block;
+    a.scales_by = a.alpha_f16 && ((per_block ? a.J / 128 : n > 1 ? a.R : 0) % 2 != 0 || reinterpret_cast<uintptr_t>(a.alpha) % 4 != 0)
+                      ? LOADED
+                      : ASYNC;
+    a.scales_f16 = a.alpha_f16 && a.scales_by == ASYNC;
+    a.scale_row = pairs && a.scales_by == ASYNC ? 2 : 4;
     a.scale_path = a.scale_row * BR;
-    a.scale_bytes = a.scale_path * n;
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {inner, static_cast<cuuint64_t>(per_block ? a.R : n), static_cast<cuuint64_t>(per_block ? n : 1)};
-    const cuuint64_t strides[2] = {inner * es, inner * es * dims[1]};
-    const cuuint32_t box[3] = {per_block ? 16 / es : BR, static_cast<cuuint32_t>(per_block ? BR : n),
-                               static_cast<cuuint32_t>(per_block ? n : 1)};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    if (enc(map, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(scales), dims,
-            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    return cudaSuccess;
-}
-
-// Plane words in boxes of 4 words (one 128-column tile) x 64 rows of every
-// path: [N][1][M][K/32], or [N][S][M][16] in the sliced order.
-cudaError_t make_planes_map(CUtensorMap* map, const BwArgs& a, int n_paths) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t words = a.sliced ? 16 : static_cast<cuuint64_t>(a.J / 32);
-    const cuuint64_t slices = a.sliced ? static_cast<cuuint64_t>((a.J + 511) / 512) : 1;
-    const cuuint64_t dims[4] = {words, static_cast<cuuint64_t>(a.R), slices, static_cast<cuuint64_t>(n_paths)};
-    const cuuint64_t strides[3] = {words * 4, words * 4 * a.R, words * 4 * a.R * slices};
-    const cuuint32_t box[4] = {4u, static_cast<cuuint32_t>(BR), 1u, static_cast<cuuint32_t>(n_paths)};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    if (enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<uint32_t*>(a.planes), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    return cudaSuccess;
 }
 
 template <int MODE, int NP, int BN, bool BF16, int FORM>
@@ -765,7 +730,7 @@ cudaError_t launch(const BwMaps& m, BwArgs& a, int cluster, cudaStream_t s) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = FORM == ONE ? 0 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, m.dy, m.c, m.s, a);
+    return cudaLaunchKernelEx(&cfg, kern, m.dy, m.c, a);
 }
 
 template <int MODE, int NP, int BN>
@@ -790,11 +755,10 @@ int bwd_tile(const BwArgs& a) {
 
 template <int NP>
 cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, cudaStream_t s) {
-    BwMaps m;
+    BwMaps m{};
     const int bn = bwd_tile(a);
+    plan_scales(a, NP);
     cudaError_t e = make_x_map(&m.dy, dY, a.R, a.N, ldd, bn == 256 ? 128 : bn);
-    if (e == cudaSuccess) e = make_planes_map(&m.c, a, NP);
-    if (e == cudaSuccess) e = plan_scales(&m.s, a, a.alpha, NP);
     if (e != cudaSuccess) return e;
     switch (bn) {
         case 32: return launch_bn<DGRAD, NP, 32>(m, a, bf16, s);
@@ -852,7 +816,7 @@ cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M,
     BwMaps m;
     cudaError_t e = make_x_map(&m.dy, dY, M, T, ldd, BR);      // boxes of 64 m x 64 t
     if (e == cudaSuccess) e = make_x8_map(&m.c, codes, K, T, 1, BR);
-    if (e == cudaSuccess) e = plan_scales(&m.s, a, scales, 1);
+    plan_scales(a, 1);
     if (e != cudaSuccess) return e;
     switch (bwd_tile(a)) {
         case 32:
