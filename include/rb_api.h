@@ -438,8 +438,15 @@ RB_API rb_status rb_unpack8(const uint8_t* codes, const float* scales, int64_t r
  * rb_gemm8 -- Y_t = W X_t for a layer kept at 8 bits, on the tcgen05 tensor
  * cores, any number of tokens:
  *     y[t][m] = sum_g xs[t][g] ws[m / 128][g] sum_{j in block g} x[t][j] w[m][j]
- * (g = 0 .. K / 128 - 1), every sum in fp32. Scales may be any fp32 values.
+ * (g = 0 .. K / 128 - 1), every sum in fp32.
  *
+ * pow2_scales  1: every scale is a power of two, as rb_pack8 writes them; the
+ *              tensor cores then apply them (16-bit outputs). A scale that is
+ *              none makes every output that it enters NaN, and rb_gemm_check
+ *              reports it. 0: any fp32 scales; each block's product is
+ *              scaled and summed in fp32 registers, which takes up to twice
+ *              as long. fp32 outputs are computed in that way whatever
+ *              pow2_scales says.
  * w, w_scales  device, [M][K] codes and [ceil(M / 128)][K / 128] scales
  *              (rb_pack8 with block_rows = 128); codes 16-byte aligned.
  * x, x_scales  device, [T][K] codes and [T][K / 128] scales (block_rows = 1).
@@ -451,7 +458,7 @@ RB_API rb_status rb_unpack8(const uint8_t* codes, const float* scales, int64_t r
  * Errors: as rb_gemm.
  */
 RB_API rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t* x, const float* x_scales, int64_t M,
-                          int64_t K, int32_t T, void* Y, rb_dtype y_dtype, int64_t ldy, void* workspace, size_t ws_bytes,
+                          int64_t K, int32_t T, int32_t pow2_scales, void* Y, rb_dtype y_dtype, int64_t ldy, void* workspace, size_t ws_bytes,
                           void* stream);
 
 /*

@@ -111,7 +111,7 @@ def load() -> ctypes.CDLL:
         lib.rb_pack8.restype = st
         lib.rb_unpack8.argtypes = [vp, vp, i64, i64, i32, vp, st, i64, vp]
         lib.rb_unpack8.restype = st
-        lib.rb_gemm8.argtypes = [vp, vp, vp, vp, i64, i64, i32, vp, st, i64, vp, sz, vp]
+        lib.rb_gemm8.argtypes = [vp, vp, vp, vp, i64, i64, i32, i32, vp, st, i64, vp, sz, vp]
         lib.rb_gemm8.restype = st
         lib.rb_gemm_wgrad.argtypes = [vp, st, i64, i64, vp, vp, i64, i32, vp, vp, st, i64, vp, sz, vp]
         lib.rb_gemm_wgrad.restype = st

@@ -529,12 +529,16 @@ def unpack8(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 1, dtyp
 
 
 def gemm8(w: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor,
-          Y: Optional[torch.Tensor] = None, y_dtype: torch.dtype = torch.float16,
+          Y: Optional[torch.Tensor] = None, y_dtype: torch.dtype = torch.float16, pow2_scales: bool = True,
           workspace: Optional[torch.Tensor] = None, check_device: bool = False) -> torch.Tensor:
     """Y[t] = W x[t] from 8-bit blocks: w, w_scales = pack8(W, block_rows=128),
-    x, x_scales = pack8(X). Any number of tokens; any fp32 scales. With
-    check_device=True the call waits for the stream and raises if the kernel
-    recorded a failure (rb_gemm_check)."""
+    x, x_scales = pack8(X). Any number of tokens.
+
+    pow2_scales=True takes scales as pack8 writes them, powers of two, which
+    the tensor cores apply; a scale that is none makes the outputs that it
+    enters NaN (and check_device raise). pow2_scales=False takes any fp32
+    scales. With check_device=True the call waits for the stream and raises
+    if the kernel recorded a failure (rb_gemm_check)."""
     lib = _lib._lib or _lib.load()
     dev = _cuda_device(w, w_scales, x, x_scales, Y, workspace)
     M, K = _blocks8(w, w_scales, 128, "w")
@@ -548,8 +552,8 @@ def gemm8(w: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: to
     else:
         _matrix(Y, "Y", (T, M), _DT8)
     workspace, ws, ws_bytes = _header(workspace, check_device, dev)
-    _call(dev, lib.rb_gemm8, w.data_ptr(), w_scales.data_ptr(), x.data_ptr(), x_scales.data_ptr(), M, K, T, Y.data_ptr(),
-          _DT8[Y.dtype], _pitch(Y), ws, ws_bytes)
+    _call(dev, lib.rb_gemm8, w.data_ptr(), w_scales.data_ptr(), x.data_ptr(), x_scales.data_ptr(), M, K, T,
+          1 if pow2_scales else 0, Y.data_ptr(), _DT8[Y.dtype], _pitch(Y), ws, ws_bytes)
     if check_device:
         _call(dev, lib.rb_gemm_check, ws)
     return Y

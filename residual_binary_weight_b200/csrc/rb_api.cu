@@ -534,7 +534,8 @@ rb_status rb_unpack8(const uint8_t* codes, const float* scales, int64_t rows, in
 }
 
 rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t* x, const float* x_scales, int64_t M, int64_t K,
-                   int32_t T, void* Y, rb_dtype y_dtype, int64_t ldy, void* workspace, size_t ws_bytes, void* stream) {
+                   int32_t T, int32_t pow2_scales, void* Y, rb_dtype y_dtype, int64_t ldy, void* workspace, size_t ws_bytes,
+                   void* stream) {
     g_last_error.clear();
     rb_status st = check_blocks8(M, K, "M");
     if (st != RB_OK) return st;
@@ -550,7 +551,9 @@ rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t* x, co
     if ((st = check_header(workspace, ws_bytes)) != RB_OK) return st;
     if (static_cast<double>((T + 127) / 128) * static_cast<double>((M + 127) / 128) >= 268435456.0)
         return fail(RB_ERR_UNSUPPORTED, "T=%d x M=%lld: 2^28 tiles or more", T, (long long)M);
-    return launched(launch_gemm8(w, w_scales, x, x_scales, M, K, T, Y, y_dtype, ldy, error_word(workspace),
+    if (pow2_scales != 0 && pow2_scales != 1) return fail(RB_ERR_INVALID_ARG, "pow2_scales=%d", pow2_scales);
+    const auto run = pow2_scales && y_dtype != RB_F32 ? launch_gemm8_mx : launch_gemm8;
+    return launched(run(w, w_scales, x, x_scales, M, K, T, Y, y_dtype, ldy, error_word(workspace),
                                  static_cast<cudaStream_t>(stream)),
                     "rb_gemm8 launch");
 }
@@ -622,6 +625,8 @@ rb_status rb_gemm_check(const void* workspace, void* stream) {
     uint32_t flag = 0;
     rb_status st = read_flags(workspace, stream, "rb_gemm_check", &flag);
     if (st != RB_OK) return st;
+    if (flag == 16u)
+        return fail(RB_ERR_DEVICE, "rb_gemm8 kernel flag 0x10: a scale is not a power of two (its products are NaN)");
     if (flag)
         return fail(RB_ERR_DEVICE, "rb_gemm kernel flag 0x%x: a pipeline wait ran out in (%s%s%s%s)", flag,
                     (flag & 1u) ? "X-tile producer " : "", (flag & 2u) ? "MMA issuer " : "",

@@ -144,6 +144,8 @@ cudaError_t launch_unpack8(const uint8_t* codes, const float* scales, int64_t ro
                            int dt, int64_t ldx, cudaStream_t s);
 cudaError_t launch_gemm8(const uint8_t* W, const float* w_scales, const uint8_t* X, const float* x_scales, int64_t M,
                          int64_t K, int T, void* Y, int y_dt, int64_t ldy, uint32_t* err, cudaStream_t s);
+cudaError_t launch_gemm8_mx(const uint8_t* W, const float* w_scales, const uint8_t* X, const float* x_scales, int64_t M,
+                            int64_t K, int T, void* Y, int y_dt, int64_t ldy, uint32_t* err, cudaStream_t s);
 cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M, const uint8_t* codes,
                               const float* scales, int64_t K, int T, const void* add, void* dW, int dw_dt, int64_t ldw,
                               uint32_t* err, cudaStream_t s);

@@ -9,10 +9,12 @@ result's terms, u = 2^-24):
   * gemm8: the products of a block are exact in fp32, 128 per block: 2^-16 D,
     then per block the factor (2 u) and one fused add (u), G of them, and the
     ranks' sums of a split (8 u): (2^-16 + (G + 10) u) D;
+    With the scales applied by the tensor cores (16-bit outputs of
+    power-of-two scales) the sum of K exact products runs through: K 2^-23 D;
   * wgrad: T products exact in fp32, `add` one more term and one more add;
   * dgrad: the operand's rounding eps / 2 (eps of dY's type) and that of its
     scales' fp32 sum (3 u), then M products: (eps / 2 + 3 u + M 2^-23) D;
-  * in both, a magnitude in D counts at least as its type's smallest normal
+  * in these, a magnitude in D counts at least as its type's smallest normal
     value: the tensor core aligns the terms of a sum by the operands' exponent
     fields, and a subnormal operand carries the smallest normal exponent, so
     a term cuts sums off at 2^-23 of max(|a|, tiny) max(|b|, tiny) (with two
@@ -160,41 +162,88 @@ def gemm8_tol(D, G):
     return (2.0 ** -16 + (G + 10) * U) * D
 
 
-def check_gemm8(rng, T, M, K, name="f16", pad=0, any_scale=False):
+def gemm8_mx_tol(w, ws, x, xs):
+    """K 2^-23 D, an e4m3 magnitude counting as at least the smallest normal, 2^-6."""
+    at = lambda c, s, r: np.maximum(np.abs(block8.e4m3_table()[c]), 2.0 ** -6) * np.repeat(np.repeat(s, 128, 1), r, 0)[:len(c)]      # noqa: E731
+    return w.shape[1] * 2.0 ** -23 * (at(x, xs, 1) @ at(w, ws, 128).T)
+
+
+def check_gemm8(rng, T, M, K, name="f16", pad=0, any_scale=False, pow2=None):
+    pow2 = not any_scale if pow2 is None else pow2
     w, ws = codes_of(rng, M, K, 128, any_scale)
     x, xs = codes_of(rng, T, K, 1, any_scale)
     ws, xs = ws * 2.0 ** -6, xs * 2.0 ** -6
     big = torch.full((T, M + pad), float("nan"), dtype=NAMES[name], device="cuda")
-    y = rb.gemm8(*dev_codes(w, ws), *dev_codes(x, xs), Y=big[:, :M], check_device=True)
+    y = rb.gemm8(*dev_codes(w, ws), *dev_codes(x, xs), Y=big[:, :M], pow2_scales=pow2, check_device=True)
     ref, D = block8.gemm8(w, ws, x, xs)
-    close(y, ref, gemm8_tol(D, K // 128), NAMES[name])
+    mx = pow2 and name != "f32"
+    close(y, ref, gemm8_mx_tol(w, ws, x, xs) if mx else gemm8_tol(D, K // 128), NAMES[name])
     assert torch.isnan(big[:, M:]).all(), "wrote past the row"
 
 
+@pytest.mark.parametrize("pow2", [True, False])
 @pytest.mark.parametrize("T", [1, 2, 9, 16, 33, 100, 128, 129, 300])
 @pytest.mark.parametrize("M,K", [(1, 128), (100, 640), (256, 1024), (515, 2176)])
-def test_gemm8_matches_oracle(T, M, K):
-    check_gemm8(np.random.default_rng(T + M + K), T, M, K)
+def test_gemm8_matches_oracle(T, M, K, pow2):
+    check_gemm8(np.random.default_rng(T + M + K), T, M, K, pow2=pow2)
 
 
 @pytest.mark.parametrize("name", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("pad", [0, 1, 8])
-def test_gemm8_types_pitches_and_any_scales(name, pad):
-    check_gemm8(np.random.default_rng(pad), 37, 331, 512, name, pad, any_scale=True)
+@pytest.mark.parametrize("any_scale", [True, False])
+def test_gemm8_types_pitches_and_any_scales(name, pad, any_scale):
+    check_gemm8(np.random.default_rng(pad), 37, 331, 512, name, pad, any_scale)
 
 
 @pytest.mark.parametrize("T,M,K,name,pad", [(1280, 4001, 256, "f16", 7), (2500, 2048, 384, "bf16", 0), (70, 40000, 128, "f32", 0),
                                             (1290, 4000, 640, "f32", 0), (300, 14336, 1152, "f16", 8), (2048, 5000, 128, "bf16", 1)])
-def test_gemm8_many_tiles(T, M, K, name, pad):
-    check_gemm8(np.random.default_rng(T), T, M, K, name, pad, any_scale=True)
+@pytest.mark.parametrize("any_scale", [True, False])
+def test_gemm8_many_tiles(T, M, K, name, pad, any_scale):
+    check_gemm8(np.random.default_rng(T), T, M, K, name, pad, any_scale)
 
 
-def test_gemm8_nan_codes_stay_in_their_row_and_column():
+@pytest.mark.parametrize("T", [5, 2100])
+def test_gemm8_scales_of_the_whole_range(T):
+    """Exponents from 2^-126 to 2^120, where their products stay in range."""
+    rng = np.random.default_rng(31)
+    M, K = 2400, 256
+    w, ws = codes_of(rng, M, K, 128)
+    x, xs = codes_of(rng, T, K, 1)
+    e = rng.integers(0, 2, (1, K // 128))
+    ws, xs = ws * np.where(e, 2.0 ** -114, 2.0 ** 117), xs * np.where(e, 2.0 ** 110, 2.0 ** -114)
+    y = rb.gemm8(*dev_codes(w, ws), *dev_codes(x, xs), y_dtype=torch.bfloat16, check_device=True)
+    close(y, block8.gemm8(w, ws, x, xs)[0], gemm8_mx_tol(w, ws, x, xs), torch.bfloat16)
+
+
+@pytest.mark.parametrize("T", [5, 2100])
+@pytest.mark.parametrize("value", [3.0, -1.0, 0.0, float("inf"), float("nan"), 1e-40])
+def test_gemm8_scales_that_are_no_powers_of_two_are_told(T, value):
+    rng = np.random.default_rng(32)
+    w, ws = codes_of(rng, 2400, 256, 128)
+    x, xs = codes_of(rng, T, 256, 1)
+    wd, wsd = dev_codes(w, ws * 2.0 ** -6)
+    xd, xsd = dev_codes(x, xs * 2.0 ** -6)
+    good = rb.gemm8(wd, wsd, xd, xsd)
+    xsd[3, 1] = value
+    with pytest.raises(rb.RbError, match="power of two"):
+        rb.gemm8(wd, wsd, xd, xsd, check_device=True)
+    y = rb.gemm8(wd, wsd, xd, xsd)
+    assert torch.isnan(y[3]).all()
+    y[3] = good[3]
+    assert torch.equal(y, good)
+    xsd[3, 1] = 1.0
+    wsd[5, 0] = value
+    y = rb.gemm8(wd, wsd, xd, xsd)
+    assert torch.isnan(y[:, 640:768]).all() and torch.isfinite(y[:, :640]).all() and torch.isfinite(y[:, 768:]).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.float16])
+def test_gemm8_nan_codes_stay_in_their_row_and_column(dt):
     rng = np.random.default_rng(8)
     w, ws = codes_of(rng, 140, 256, 128)
     x, xs = codes_of(rng, 20, 256, 1)
     w[133, 200], x[3, 5] = 0x7F, 0xFF
-    y = f64(rb.gemm8(*dev_codes(w, ws * 2.0 ** -6), *dev_codes(x, xs * 2.0 ** -6), y_dtype=torch.float32))
+    y = f64(rb.gemm8(*dev_codes(w, ws * 2.0 ** -6), *dev_codes(x, xs * 2.0 ** -6), y_dtype=dt))
     bad = np.isnan(y)
     assert bad[3].all() and bad[:, 133].all()
     bad[3], bad[:, 133] = False, False
@@ -399,8 +448,7 @@ def test_eight_bit_layer_next_to_its_checkpoint():
     x, xs = rb.pack8(X)
     y = rb.gemm8(w, ws, x, xs, y_dtype=torch.bfloat16, check_device=True)
     wh, wsh, xh, xsh = (t.view(torch.uint8).cpu().numpy() if t.dtype == torch.float8_e4m3fn else f64(t) for t in (w, ws, x, xs))
-    ref, D = block8.gemm8(wh, wsh, xh, xsh)
-    close(y, ref, gemm8_tol(D, 3), torch.bfloat16)
+    close(y, block8.gemm8(wh, wsh, xh, xsh)[0], gemm8_mx_tol(wh, wsh, xh, xsh), torch.bfloat16)
     dw = rb.gemm_wgrad(y, x, xs, check_device=True)
     ref, D = block8.wgrad(f64(y), block8.unpack8(xh, xsh, 1))
     close(dw, ref, 41 * 2.0 ** -23 * D, torch.float32)

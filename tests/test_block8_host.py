@@ -51,11 +51,11 @@ def test_unpack8_refusals():
 
 
 def test_gemm8_refusals():
-    call = _caller("rb_gemm8", ["w", "ws", "x", "xs", "M", "K", "T", "Y", "dt", "ldy", "wk", "wb", "s"],
-                   (FAKE, FAKE, FAKE, FAKE, 100, 256, 5, FAKE, F16, 100, FAKE, 256, None))
+    call = _caller("rb_gemm8", ["w", "ws", "x", "xs", "M", "K", "T", "p2", "Y", "dt", "ldy", "wk", "wb", "s"],
+                   (FAKE, FAKE, FAKE, FAKE, 100, 256, 5, 1, FAKE, F16, 100, FAKE, 256, None))
     for k in ("w", "ws", "x", "xs", "Y"):
         assert call(**{k: None}) == "RB_ERR_INVALID_ARG", k
-    assert call(dt=3) == call(M=0) == call(ldy=99) == "RB_ERR_INVALID_ARG"
+    assert call(dt=3) == call(M=0) == call(ldy=99) == call(p2=2) == "RB_ERR_INVALID_ARG"
     assert call(T=0) == call(T=(1 << 22) + 1) == call(K=64) == "RB_ERR_UNSUPPORTED"
     assert call(w=FAKE + 4) == call(x=FAKE + 8) == call(ws=FAKE + 2) == call(xs=FAKE + 1) == "RB_ERR_ALIGNMENT"
     assert call(Y=FAKE + 1) == call(Y=FAKE + 2, dt=F32) == "RB_ERR_ALIGNMENT"
