@@ -146,7 +146,9 @@ __device__ __forceinline__ uint2 encode(const Raw8<DT>& r, int n, bool odd) {
 
 // One scale per 128 columns of a row: a half warp per block, UNITS blocks of
 // each half warp loaded before the first is used.
-template <int DT>
+// DENSE: rows follow one another without a gap, so a block's place needs no
+// division.
+template <int DT, bool DENSE>
 __global__ void __launch_bounds__(THREADS)
 pack8_rows_kernel(const char* X, int64_t ldx, uint32_t blocks, uint32_t G, uint8_t* codes, float* scales) {
     const uint32_t lane = threadIdx.x & 15u;
@@ -157,8 +159,12 @@ pack8_rows_kernel(const char* X, int64_t ldx, uint32_t blocks, uint32_t G, uint8
     for (int u = 0; u < UNITS; ++u) {
         const uint32_t b = b0 + u * stride;
         if (b < blocks) {
-            const uint32_t row = b / G;
-            r[u].load(X + (static_cast<int64_t>(row) * ldx + (b - row * G) * 128u + lane * 8u) * elt_bytes<DT>());
+            int64_t at = static_cast<int64_t>(b) * 128;
+            if constexpr (!DENSE) {
+                const uint32_t row = b / G;
+                at = static_cast<int64_t>(row) * ldx + (b - row * G) * 128u;
+            }
+            r[u].load(X + (at + lane * 8u) * elt_bytes<DT>());
         } else {
             r[u].zero();
         }
@@ -308,9 +314,13 @@ cudaError_t launch_pack8(const void* X, int dt, int64_t ldx, int64_t rows, int64
     if (block_rows == 1) {
         const uint32_t blocks = static_cast<uint32_t>(rows) * G;
         const unsigned grid = grid_for(blocks);
-        if (dt == B8_F16) pack8_rows_kernel<B8_F16><<<grid, THREADS, 0, s>>>(x, ldx, blocks, G, codes, scales);
-        else if (dt == B8_BF16) pack8_rows_kernel<B8_BF16><<<grid, THREADS, 0, s>>>(x, ldx, blocks, G, codes, scales);
-        else pack8_rows_kernel<B8_F32><<<grid, THREADS, 0, s>>>(x, ldx, blocks, G, codes, scales);
+        auto go = [&](auto dense_kernel, auto kernel) {
+            if (ldx == K) dense_kernel<<<grid, THREADS, 0, s>>>(x, ldx, blocks, G, codes, scales);
+            else kernel<<<grid, THREADS, 0, s>>>(x, ldx, blocks, G, codes, scales);
+        };
+        if (dt == B8_F16) go(pack8_rows_kernel<B8_F16, true>, pack8_rows_kernel<B8_F16, false>);
+        else if (dt == B8_BF16) go(pack8_rows_kernel<B8_BF16, true>, pack8_rows_kernel<B8_BF16, false>);
+        else go(pack8_rows_kernel<B8_F32, true>, pack8_rows_kernel<B8_F32, false>);
     } else {
         const unsigned grid = static_cast<unsigned>((rows + 127) / 128) * G;
         if (dt == B8_F16) pack8_tile_kernel<B8_F16><<<grid, THREADS, 0, s>>>(x, ldx, rows, G, codes, scales);

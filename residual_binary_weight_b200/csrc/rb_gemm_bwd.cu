@@ -53,7 +53,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int EPI_WARPS = 4, EXP_WARP0 = 4, GROUP_WARPS = 4;
+constexpr int EPI_WARPS = 4, GROUP_WARPS = 4;
 constexpr int BR = 64;                          // rows r per stage
 constexpr uint32_t A_BYTES = 128 * BR * 2;      // two chunks of [64 r][64 j]
 constexpr uint32_t CHUNK = 64 * BR * 2;         // 8 KB
@@ -75,8 +75,11 @@ struct BwCfg {
     static constexpr uint32_t B_BYTES = BNC * BR * 2;
     static constexpr uint32_t C_BYTES = MODE == WGRAD ? 128 * BR : NP * 16 * BR;
     static constexpr uint32_t S_BYTES = NP * 16 * BR;      // most bytes of a stage's scales
-    // expansion groups: a stage's MMAs take 2 BN cycles, a group's stage about 1000
-    static constexpr int GROUPS = 3;
+    // Expansion groups of four warps: a group's stage takes about 1700 cycles. In
+    // a SPLIT tile the epilogue's warps have nothing else to do until the last
+    // stage and are a fourth group.
+    static constexpr int GROUPS = FORM == SPLIT ? 4 : 3;
+    static constexpr int EXP_WARP0 = FORM == SPLIT ? 0 : EPI_WARPS;
     static constexpr int B_WARP = EXP_WARP0 + GROUPS * GROUP_WARPS, MMA_WARP = B_WARP + 1, C_WARP = B_WARP + 2, C_WARPS = 2;
     static constexpr int THREADS = 32 * (C_WARP + C_WARPS);
     static constexpr int ST = MODE == WGRAD || NP > 2 ? 5 : 6, CS = ST;
@@ -100,6 +103,7 @@ struct BwArgs {
     const void* add;            // wgrad, may be null
     void* out;
     int64_t R, N, J, ldo;       // contraction, output rows, output columns (K)
+    int bn;                     // output rows per tile (BN, or less in a pair of dgrad)
     int j_tiles, n_tiles;
     int out_dt;
     bool sliced, alpha_f16, g128;
@@ -312,7 +316,7 @@ __global__ void __launch_bounds__(BwCfg<MODE, NP, BN, FORM>::THREADS, 1)
 gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap cmap, BwArgs a) {
     using C = BwCfg<MODE, NP, BN, FORM>;
     constexpr int ST = C::ST, CS = C::CS, GROUPS = C::GROUPS;
-    constexpr int B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP;
+    constexpr int EXP_WARP0 = C::EXP_WARP0, B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP;
     constexpr int C_WARPS = C::C_WARPS;
     extern __shared__ __align__(1024) unsigned char dsm[];
     __shared__ __align__(8) uint64_t bars[C::BARS];
@@ -364,6 +368,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     fence_after();
     const uint32_t tmem = tmem_slot;
 
+    const int bn = FORM == PAIR ? a.bn : BN;
     const int64_t nr = (a.R + BR - 1) / BR;
     const int r_lo = FORM == SPLIT ? static_cast<int>(nr * rank / size) : 0;
     const int r_hi = FORM == SPLIT ? static_cast<int>(nr * (rank + 1) / size) : static_cast<int>(nr);
@@ -376,19 +381,57 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     auto j_tile = [&](int u) { return FORM == PAIR ? 2 * (u % jw) + static_cast<int>(rank) : u % jw; };
     auto n_tile = [&](int u) { return u / jw; };
 
+    auto epilogue = [&] {
+        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+        const int column = MODE == DGRAD ? (lane >> 1) + (lane & 1) * 16 : lane;      // of this tensor-memory lane
+        int tile = 0;
+        for (int u = u0; u < units; u += u_step, ++tile) {
+            const int b = tile & 1;
+            const int64_t j = static_cast<int64_t>(j_tile(u)) * 128 + warp * 32 + column;
+            const int64_t n0 = static_cast<int64_t>(n_tile(u)) * bn;
+            const bool mine = FORM != PAIR || j < a.J;
+            if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(tile >> 1) & 1u, abort_flag, err, 8u)) ||
+                *abort_flag)
+                break;
+            fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < bn; c0 += 32) {
+                uint32_t v[32];
+                tmem_load<32>(tmem + lanes + static_cast<uint32_t>(b * BN + c0), v);
+                if constexpr (FORM == SPLIT) {
+                    float* buf = reinterpret_cast<float*>(dsm + (tiles - smem_addr(dsm))) + c0 * 128 + warp * 32 + column;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) buf[i * 128] = __uint_as_float(v[i]);
+                } else {
+                    const int left = mine ? static_cast<int>(min(static_cast<int64_t>(min(32, bn - c0)), a.N - n0 - c0)) : 0;
+                    const int64_t at = (n0 + c0) * a.ldo + j;
+                    const void* add = MODE == WGRAD ? a.add : nullptr;
+                    if (a.out_dt == B8_F32) store_rows<float>(a.out, add, at, a.ldo, left, v);
+                    else if (a.out_dt == B8_F16) store_rows<__half>(a.out, add, at, a.ldo, left, v);
+                    else store_rows<__nv_bfloat16>(a.out, add, at, a.ldo, left, v);
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (FORM == PAIR && rank == 1) mbar_arrive_remote(acc_empty(b), 0);
+                else mbar_arrive(acc_empty(b));
+            }
+        }
+    };
     if (warp == B_WARP) {
         if (lane == 0) {
             Ring<ST> q;
             int it = 0;
             bool ok = true;
             for (int u = u0; u < units && ok; u += u_step) {
-                const int n0 = n_tile(u) * BN + (FORM == PAIR ? static_cast<int>(rank) * C::BNC : 0);
+                const int n0 = n_tile(u) * bn + (FORM == PAIR ? static_cast<int>(rank) * (bn / 2) : 0);
                 for (int rb = r_lo; rb < r_hi; ++rb, ++it, q.next()) {
                     if (!mbar_wait(empty_bar(q.slot), q.ph ^ 1u, abort_flag, err, 1u)) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(full_bar(q.slot), C::B_BYTES);
+                    mbar_arrive_expect_tx(full_bar(q.slot), static_cast<uint32_t>(FORM == PAIR ? bn / 2 : bn) * (BR * 2));
                     if constexpr (MODE == DGRAD) {
                         tma_load_2d(b_tile(q.slot), &dmap, rb * BR, n0, full_bar(q.slot));
                     } else {
@@ -511,7 +554,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             }
         }
     } else if (warp == MMA_WARP) {
-        constexpr uint32_t idesc = idesc_bw(BN, BF16, MODE == WGRAD, FORM == PAIR ? 256 : BM);
+        const uint32_t idesc = idesc_bw(bn, BF16, MODE == WGRAD, FORM == PAIR ? 256 : BM);
         auto commit = [](uint32_t bar) {
             if constexpr (FORM == PAIR) umma2_commit(bar);
             else umma_commit(bar);
@@ -555,6 +598,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         if (!ok)
             for (int i = tile - 1; i >= 0 && i >= tile - 2; --i) mbar_drain(acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u);
     } else if (warp >= EXP_WARP0) {
+        // (in a SPLIT tile warps 0-3, too)
         // A thread expands two rows of a stage, 32 columns of each. wgrad: warp wq
         // takes columns 32 wq.. of rows lane and lane + 32. dgrad: 4 lanes
         // share a row (its 4 words, one LDS of 128 contiguous bytes per 8
@@ -626,50 +670,17 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             }
         }
     } else {
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        const int column = MODE == DGRAD ? (lane >> 1) + (lane & 1) * 16 : lane;      // of this tensor-memory lane
-        int tile = 0;
-        for (int u = u0; u < units; u += u_step, ++tile) {
-            const int b = tile & 1;
-            const int64_t j = static_cast<int64_t>(j_tile(u)) * 128 + warp * 32 + column;
-            const int64_t n0 = static_cast<int64_t>(n_tile(u)) * BN;
-            const bool mine = FORM != PAIR || j < a.J;
-            if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(tile >> 1) & 1u, abort_flag, err, 8u)) ||
-                *abort_flag)
-                break;
-            fence_after();
-#pragma unroll 1
-            for (int c0 = 0; c0 < BN; c0 += 32) {
-                uint32_t v[32];
-                tmem_load<32>(tmem + lanes + static_cast<uint32_t>(b * BN + c0), v);
-                if constexpr (FORM == SPLIT) {
-                    float* buf = reinterpret_cast<float*>(dsm + (tiles - smem_addr(dsm))) + c0 * 128 + warp * 32 + column;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) buf[i * 128] = __uint_as_float(v[i]);
-                } else {
-                    const int left = mine ? static_cast<int>(min(static_cast<int64_t>(32), a.N - n0 - c0)) : 0;
-                    const int64_t at = (n0 + c0) * a.ldo + j;
-                    const void* add = MODE == WGRAD ? a.add : nullptr;
-                    if (a.out_dt == B8_F32) store_rows<float>(a.out, add, at, a.ldo, left, v);
-                    else if (a.out_dt == B8_F16) store_rows<__half>(a.out, add, at, a.ldo, left, v);
-                    else store_rows<__nv_bfloat16>(a.out, add, at, a.ldo, left, v);
-                }
-            }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (FORM == PAIR && rank == 1) mbar_arrive_remote(acc_empty(b), 0);
-                else mbar_arrive(acc_empty(b));
-            }
-        }
+        epilogue();
     }
+    if constexpr (FORM == SPLIT)
+        if (warp < EPI_WARPS) epilogue();
     __syncwarp();
     fence_before();
     if constexpr (FORM == SPLIT) {
         cluster_sync();
         // the CTAs of the cluster take the output rows in turn and add the ranks' sums in rank order
         const int64_t j = static_cast<int64_t>(j_tile(u0)) * 128 + (threadIdx.x & 127);
-        const int64_t n0 = static_cast<int64_t>(n_tile(u0)) * BN;
+        const int64_t n0 = static_cast<int64_t>(n_tile(u0)) * bn;
         const int rows = static_cast<int>(min(static_cast<int64_t>(BN), a.N - n0));
         if (*abort_flag == 0u && threadIdx.x < 384) {
             for (int c = static_cast<int>(rank) * 3 + (threadIdx.x >> 7); c < rows; c += static_cast<int>(size) * 3) {
@@ -758,7 +769,23 @@ cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, c
     BwMaps m{};
     const int bn = bwd_tile(a);
     plan_scales(a, NP);
-    cudaError_t e = make_x_map(&m.dy, dY, a.R, a.N, ldd, bn == 256 ? 128 : bn);
+    a.bn = bn;
+    if (bn == 256) {
+        // a pair's tile of 128 to 256 tokens: the least time over all waves of
+        // tiles; a stage's MMAs take 2 bn cycles, issuing them about 350. (16
+        // column tiles of pairs x 1184 tokens are 80 tiles of 256, two waves on 74
+        // pairs, or 128 of 160, also two: 163 -> 113 us.)
+        const int64_t pairs = device_sm_count() / 2, jw = (a.j_tiles + 1) / 2;
+        int64_t best = 0;
+        for (int n = 256; n >= 128; n -= 16) {
+            const int64_t waves = (jw * ((a.N + n - 1) / n) + pairs - 1) / pairs, cost = waves * std::max(2 * n, 350);
+            if (best == 0 || cost < best) {
+                best = cost;
+                a.bn = n;
+            }
+        }
+    }
+    cudaError_t e = make_x_map(&m.dy, dY, a.R, a.N, ldd, bn == 256 ? a.bn / 2 : bn);
     if (e != cudaSuccess) return e;
     switch (bn) {
         case 32: return launch_bn<DGRAD, NP, 32>(m, a, bf16, s);
@@ -766,7 +793,7 @@ cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, c
         case 128: return launch_bn<DGRAD, NP, 128>(m, a, bf16, s);
         default: break;
     }
-    a.n_tiles = static_cast<int>((a.N + 255) / 256);
+    a.n_tiles = static_cast<int>((a.N + a.bn - 1) / a.bn);
     return bf16 ? launch<DGRAD, NP, 256, true, PAIR>(m, a, 2, s) : launch<DGRAD, NP, 256, false, PAIR>(m, a, 2, s);
 }
 
@@ -824,6 +851,7 @@ cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M,
         case 128: return launch_bn<WGRAD, 1, 128>(m, a, bf16, s);
         default: break;
     }
+    a.bn = 256;
     a.n_tiles = static_cast<int>((M + 255) / 256);
     return bf16 ? launch<WGRAD, 1, 256, true, PAIR>(m, a, 2, s) : launch<WGRAD, 1, 256, false, PAIR>(m, a, 2, s);
 }
