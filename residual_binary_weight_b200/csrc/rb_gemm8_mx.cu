@@ -220,7 +220,7 @@ gemm8_mx_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
         const uint64_t ad0 = smem_desc(a_tile(0)), bd0 = smem_desc(b_tile(0));
         int s = 0, tile = 0;
         uint32_t ph = 0u;
-        bool ok = true;
+        bool ok = true, ready = false;
         auto commit = [](uint32_t bar) {
             if constexpr (FORM == PAIR) umma2_commit(bar);
             else umma_commit(bar);
@@ -231,25 +231,29 @@ gemm8_mx_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant_
             const uint32_t d = tmem + static_cast<uint32_t>(b * C::BN);
             ok = __all_sync(FULL_MASK, mbar_wait(acc_empty(b), aph, abort_flag, err, 2u));
             for (int g = g_lo; g < g_hi && ok; ++g) {
-                if (!__all_sync(FULL_MASK, mbar_wait(full_bar(s), ph, abort_flag, err, 2u))) {
+                if (!__all_sync(FULL_MASK, ready || mbar_wait(full_bar(s), ph, abort_flag, err, 2u))) {
                     ok = false;
                     break;
                 }
-                fence_after();
-                const uint64_t ad = ad0 + static_cast<uint32_t>(s) * (a_bytes >> 4), bd = bd0 + static_cast<uint32_t>(s) * (C::B_BYTES >> 4);
-                const uint32_t sf = tmem + static_cast<uint32_t>(C::SF0 + s * C::SF_COLS);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_mx<FORM == PAIR>(d, ad + 2u * kk, bd + 2u * kk, idesc, (g > g_lo || kk > 0) ? 1u : 0u, sf, sf + 4u);
-                    commit(empty_bar(s));
-                    if (g + 1 == g_hi) commit(acc_full(b));
-                }
-                __syncwarp();
+                const int now = s;
                 if (++s == stages) {
                     s = 0;
                     ph ^= 1u;
                 }
+                // the next stage's barrier is looked at while this one's MMAs are issued
+                ready = mbar_test(full_bar(s), ph);
+                fence_after();
+                const uint64_t ad = ad0 + static_cast<uint32_t>(now) * (a_bytes >> 4);
+                const uint64_t bd = bd0 + static_cast<uint32_t>(now) * (C::B_BYTES >> 4);
+                const uint32_t sf = tmem + static_cast<uint32_t>(C::SF0 + now * C::SF_COLS);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_mx<FORM == PAIR>(d, ad + 2u * kk, bd + 2u * kk, idesc, (g > g_lo || kk > 0) ? 1u : 0u, sf, sf + 4u);
+                    commit(empty_bar(now));
+                    if (g + 1 == g_hi) commit(acc_full(b));
+                }
+                __syncwarp();
             }
             // after an abort the teardown waits for it
             if (!ok && elect_one()) commit(acc_full(b));

@@ -21,9 +21,8 @@
 // 550 with separate barriers for A and B, more than the 512 that the MMAs
 // of a 256-wide tile last.
 //
-// Roles: warps 0-3 epilogue, then two or three groups of four expansion warps
-// that take the stages in turn, one warp each for B loads and MMAs, and two for
-// C.
+// Roles: warp 0 MMAs, 1 B loads, 2-3 C copies, 4-7 epilogue, then groups of four
+// expansion warps that take the stages in turn.
 // Three forms:
 //   ONE    a CTA walks its 128 x BN tiles with two accumulators, so the
 //          epilogue of a tile overlaps the next tile's MMAs;
@@ -79,9 +78,9 @@ struct BwCfg {
     // a SPLIT tile the epilogue's warps have nothing else to do until the last
     // stage and are a fourth group.
     static constexpr int GROUPS = FORM == SPLIT ? 4 : 3;
-    static constexpr int EXP_WARP0 = FORM == SPLIT ? 0 : EPI_WARPS;
-    static constexpr int B_WARP = EXP_WARP0 + GROUPS * GROUP_WARPS, MMA_WARP = B_WARP + 1, C_WARP = B_WARP + 2, C_WARPS = 2;
-    static constexpr int THREADS = 32 * (C_WARP + C_WARPS);
+    static constexpr int MMA_WARP = 0, B_WARP = 1, C_WARP = 2, C_WARPS = 2, EPI_WARP0 = 4;
+    static constexpr int EXP_WARP0 = FORM == SPLIT ? EPI_WARP0 : EPI_WARP0 + EPI_WARPS;
+    static constexpr int THREADS = 32 * (EXP_WARP0 + GROUPS * GROUP_WARPS);
     static constexpr int ST = MODE == WGRAD || NP > 2 ? 5 : 6, CS = ST;
     static constexpr uint32_t STAGE = A_BYTES + B_BYTES, TILES = ST * STAGE + CS * (C_BYTES + S_BYTES);
     static constexpr int BARS = 2 * (ST + CS) + 4;
@@ -316,7 +315,7 @@ __global__ void __launch_bounds__(BwCfg<MODE, NP, BN, FORM>::THREADS, 1)
 gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap cmap, BwArgs a) {
     using C = BwCfg<MODE, NP, BN, FORM>;
     constexpr int ST = C::ST, CS = C::CS, GROUPS = C::GROUPS;
-    constexpr int EXP_WARP0 = C::EXP_WARP0, B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP;
+    constexpr int EPI_WARP0 = C::EPI_WARP0, EXP_WARP0 = C::EXP_WARP0, B_WARP = C::B_WARP, MMA_WARP = C::MMA_WARP, C_WARP = C::C_WARP;
     constexpr int C_WARPS = C::C_WARPS;
     extern __shared__ __align__(1024) unsigned char dsm[];
     __shared__ __align__(8) uint64_t bars[C::BARS];
@@ -382,12 +381,13 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     auto n_tile = [&](int u) { return u / jw; };
 
     auto epilogue = [&] {
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+        const int q = warp - EPI_WARP0;          // lane quarter
+        const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
         const int column = MODE == DGRAD ? (lane >> 1) + (lane & 1) * 16 : lane;      // of this tensor-memory lane
         int tile = 0;
         for (int u = u0; u < units; u += u_step, ++tile) {
             const int b = tile & 1;
-            const int64_t j = static_cast<int64_t>(j_tile(u)) * 128 + warp * 32 + column;
+            const int64_t j = static_cast<int64_t>(j_tile(u)) * 128 + q * 32 + column;
             const int64_t n0 = static_cast<int64_t>(n_tile(u)) * bn;
             const bool mine = FORM != PAIR || j < a.J;
             if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(tile >> 1) & 1u, abort_flag, err, 8u)) ||
@@ -399,7 +399,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 uint32_t v[32];
                 tmem_load<32>(tmem + lanes + static_cast<uint32_t>(b * BN + c0), v);
                 if constexpr (FORM == SPLIT) {
-                    float* buf = reinterpret_cast<float*>(dsm + (tiles - smem_addr(dsm))) + c0 * 128 + warp * 32 + column;
+                    float* buf = reinterpret_cast<float*>(dsm + (tiles - smem_addr(dsm))) + c0 * 128 + q * 32 + column;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) buf[i * 128] = __uint_as_float(v[i]);
                 } else {
@@ -451,7 +451,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 for (int i = it - 1; i >= 0 && i >= it - ST; --i)
                     mbar_drain(empty_bar(i % ST), static_cast<uint32_t>(i / ST) & 1u);
         }
-    } else if (warp >= C_WARP) {
+    } else if (warp >= C_WARP && warp < C_WARP + C_WARPS) {
         const int mine = warp - C_WARP;
         Ring<CS> q;
         q.next(mine);
@@ -561,7 +561,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         };
         Ring<ST> q;
         int tile = 0;
-        bool ok = true;
+        bool ok = true, ready = false;
         // the low words of the descriptors of slot 0 (the high words do not change)
         const uint64_t ad0 = smem_desc_mn(a_tile(0)), bd0 = MODE == DGRAD ? smem_desc(b_tile(0)) : smem_desc_mn(b_tile(0));
         // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
@@ -570,13 +570,17 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             const int b = tile & 1;
             const uint32_t aph = (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u, d = tmem + static_cast<uint32_t>(b * BN);
             ok = __all_sync(FULL_MASK, mbar_wait(acc_empty(b), aph, abort_flag, err, 2u));
-            for (int rb = r_lo; rb < r_hi && ok; ++rb, q.next()) {
-                if (!__all_sync(FULL_MASK, mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u))) {
+            for (int rb = r_lo; rb < r_hi && ok; ++rb) {
+                if (!__all_sync(FULL_MASK, ready || mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u))) {
                     ok = false;
                     break;
                 }
+                const int slot = q.slot;
+                q.next();
+                // the next stage's barrier is looked at while this one's MMAs are issued
+                ready = mbar_test(full_bar(q.slot), q.ph);
                 fence_after();
-                const uint32_t off = static_cast<uint32_t>(q.slot) * (C::STAGE >> 4);
+                const uint32_t off = static_cast<uint32_t>(slot) * (C::STAGE >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < BR / 16; ++kk) {
@@ -585,7 +589,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                         if constexpr (FORM == PAIR) umma2_f16(d, ad, bd, idesc, more);
                         else umma_f16(d, ad, bd, idesc, more);
                     }
-                    commit(empty_bar(q.slot));
+                    commit(empty_bar(slot));
                     if (rb + 1 == r_hi) commit(acc_full(b));
                 }
                 __syncwarp();
@@ -598,7 +602,6 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         if (!ok)
             for (int i = tile - 1; i >= 0 && i >= tile - 2; --i) mbar_drain(acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u);
     } else if (warp >= EXP_WARP0) {
-        // (in a SPLIT tile warps 0-3, too)
         // A thread expands two rows of a stage, 32 columns of each. wgrad: warp wq
         // takes columns 32 wq.. of rows lane and lane + 32. dgrad: 4 lanes
         // share a row (its 4 words, one LDS of 128 contiguous bytes per 8
@@ -673,7 +676,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         epilogue();
     }
     if constexpr (FORM == SPLIT)
-        if (warp < EPI_WARPS) epilogue();
+        if (warp >= EPI_WARP0 && warp < EPI_WARP0 + EPI_WARPS) epilogue();
     __syncwarp();
     fence_before();
     if constexpr (FORM == SPLIT) {
@@ -744,47 +747,69 @@ cudaError_t launch(const BwMaps& m, BwArgs& a, int cluster, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kern, m.dy, m.c, a);
 }
 
+// A stage takes about 600 cycles (the MMA warp's waits, issue and commit; the
+// expansion) or its MMAs' 2 bn in a pair, whichever is more. Time in stages of
+// the two ways to cover N rows of dY of more than 64:
+constexpr int64_t STAGE_CYCLES = 600;
+
+// 256-wide tiles of CTA pairs, of which a dgrad tile may use only bn rows (128
+// to 256 by 16): the bn with the least time over all waves of tiles
+int64_t pair_cycles(const BwArgs& a, int* bn, bool narrow) {
+    const int64_t pairs = device_sm_count() / 2, jw = (a.j_tiles + 1) / 2, nr = (a.R + BR - 1) / BR;
+    int64_t best = 0;
+    for (int n = 256; n >= (narrow ? 128 : 256); n -= 16) {
+        const int64_t waves = (jw * ((a.N + n - 1) / n) + pairs - 1) / pairs;
+        const int64_t cycles = waves * nr * std::max<int64_t>(2 * n, STAGE_CYCLES);
+        if (best == 0 || cycles < best) {
+            best = cycles;
+            *bn = n;
+        }
+    }
+    return best;
+}
+
+// CTAs that share a tile's rows r
+int split_of(int64_t units, int64_t nr) {
+    int split = 1;
+    while (split < 8 && units * (split + 1) <= device_sm_count() && split < nr) ++split;
+    return split;
+}
+
+// 128-wide tiles, of one CTA or split
+int64_t one_cycles(const BwArgs& a) {
+    const int64_t units = a.j_tiles * ((a.N + 127) / 128), nr = (a.R + BR - 1) / BR, sms = device_sm_count();
+    const int split = split_of(units, nr);
+    return split > 1 ? (nr + split - 1) / split * STAGE_CYCLES : (units + sms - 1) / sms * nr * STAGE_CYCLES;
+}
+
+// Rows of the dY tile: the narrowest that covers N; 256 is a CTA pair's. (600
+// tokens x 14336 x 4096, dgrad: 160 tiles of 128, two waves of 148, take 148 us; 64
+// pairs' tiles of 160 one wave.)
+int bwd_tile(BwArgs& a, bool narrow) {
+    a.bn = a.N <= 32 ? 32 : a.N <= 64 ? 64 : 128;
+    int bn = 0;
+    if (a.N > 128 && pair_cycles(a, &bn, narrow) < one_cycles(a)) {
+        a.bn = bn;
+        return 256;
+    }
+    return a.bn;
+}
+
 template <int MODE, int NP, int BN>
 cudaError_t launch_bn(const BwMaps& m, BwArgs& a, bool bf16, cudaStream_t s) {
     a.n_tiles = static_cast<int>((a.N + BN - 1) / BN);
     const int64_t units = static_cast<int64_t>(a.j_tiles) * a.n_tiles, nr = (a.R + BR - 1) / BR;
-    int split = 1;
-    while (split < 8 && units * (split + 1) <= device_sm_count() && split < nr) ++split;
+    const int split = split_of(units, nr);
     if (split > 1)
         return bf16 ? launch<MODE, NP, BN, true, SPLIT>(m, a, split, s) : launch<MODE, NP, BN, false, SPLIT>(m, a, split, s);
     return bf16 ? launch<MODE, NP, BN, true, ONE>(m, a, 1, s) : launch<MODE, NP, BN, false, ONE>(m, a, 1, s);
 }
 
-// Rows of the dY tile: the narrowest that covers N; 256, as a CTA pair's, where
-// there is at least one 256 x 256 tile for each pair of SMs (otherwise more,
-// smaller tiles, or the split of their rows r, keep more SMs busy).
-int bwd_tile(const BwArgs& a) {
-    if (a.N <= 32) return 32;
-    if (a.N <= 64) return 64;
-    return a.N <= 128 || a.j_tiles * ((a.N + 127) / 128) < 2 * device_sm_count() ? 128 : 256;
-}
-
 template <int NP>
 cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, cudaStream_t s) {
     BwMaps m{};
-    const int bn = bwd_tile(a);
+    const int bn = bwd_tile(a, true);
     plan_scales(a, NP);
-    a.bn = bn;
-    if (bn == 256) {
-        // a pair's tile of 128 to 256 tokens: the least time over all waves of
-        // tiles; a stage's MMAs take 2 bn cycles, issuing them about 350. (16
-        // column tiles of pairs x 1184 tokens are 80 tiles of 256, two waves on 74
-        // pairs, or 128 of 160, also two: 163 -> 113 us.)
-        const int64_t pairs = device_sm_count() / 2, jw = (a.j_tiles + 1) / 2;
-        int64_t best = 0;
-        for (int n = 256; n >= 128; n -= 16) {
-            const int64_t waves = (jw * ((a.N + n - 1) / n) + pairs - 1) / pairs, cost = waves * std::max(2 * n, 350);
-            if (best == 0 || cost < best) {
-                best = cost;
-                a.bn = n;
-            }
-        }
-    }
     cudaError_t e = make_x_map(&m.dy, dY, a.R, a.N, ldd, bn == 256 ? a.bn / 2 : bn);
     if (e != cudaSuccess) return e;
     switch (bn) {
@@ -845,13 +870,12 @@ cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M,
     if (e == cudaSuccess) e = make_x8_map(&m.c, codes, K, T, 1, BR);
     plan_scales(a, 1);
     if (e != cudaSuccess) return e;
-    switch (bwd_tile(a)) {
+    switch (bwd_tile(a, false)) {
         case 32:
         case 64: return launch_bn<WGRAD, 1, 64>(m, a, bf16, s);
         case 128: return launch_bn<WGRAD, 1, 128>(m, a, bf16, s);
         default: break;
     }
-    a.bn = 256;
     a.n_tiles = static_cast<int>((M + 255) / 256);
     return bf16 ? launch<WGRAD, 1, 256, true, PAIR>(m, a, 2, s) : launch<WGRAD, 1, 256, false, PAIR>(m, a, 2, s);
 }
