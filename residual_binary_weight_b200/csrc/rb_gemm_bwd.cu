@@ -73,15 +73,20 @@ struct BwCfg {
     static constexpr int BNC = FORM == PAIR ? BN / 2 : BN;      // rows of the dY tile in this CTA
     static constexpr uint32_t B_BYTES = BNC * BR * 2;
     static constexpr uint32_t C_BYTES = MODE == WGRAD ? 128 * BR : NP * 16 * BR;
-    static constexpr uint32_t S_BYTES = NP * 16 * BR;      // most bytes of a stage's scales
-    // Expansion groups of four warps: a group's stage takes about 1700 cycles. In
-    // a SPLIT tile the epilogue's warps have nothing else to do until the last
-    // stage and are a fourth group.
-    static constexpr int GROUPS = FORM == SPLIT ? 4 : 3;
-    static constexpr int MMA_WARP = 0, B_WARP = 1, C_WARP = 2, C_WARPS = 2, EPI_WARP0 = 4;
-    static constexpr int EXP_WARP0 = FORM == SPLIT ? EPI_WARP0 : EPI_WARP0 + EPI_WARPS;
+    static constexpr uint32_t S_BYTES = NP * 4 * BR;       // most bytes of a stage's scales
+    // Expansion groups of four warps (a group's stage takes about 1700 cycles)
+    // and copying warps.
+    static constexpr int GROUPS = 3, C_WARPS = MODE == WGRAD ? 1 : 2;
+    static constexpr int MMA_WARP = 0, B_WARP = 1, C_WARP = 2, EPI_WARP0 = 4, EXP_WARP0 = EPI_WARP0 + EPI_WARPS;
     static constexpr int THREADS = 32 * (EXP_WARP0 + GROUPS * GROUP_WARPS);
-    static constexpr int ST = MODE == WGRAD || NP > 2 ? 5 : 6, CS = ST;
+    // Slots are a multiple of the groups (and copying warps) that take them in
+    // turn, so that a slot always belongs to the same one, which then waits
+    // for every phase of its barriers. Otherwise a group could wait for a
+    // slot's use while the use before, another group's, was still being
+    // filled (copies land in any order), and a parity wait for the phase
+    // after an open one returns at once.
+    static constexpr int ST = 6, CS = MODE == WGRAD ? 3 : 6;
+    static_assert(ST % GROUPS == 0 && CS % GROUPS == 0 && CS % C_WARPS == 0, "a waiter would miss phases of its barriers");
     static constexpr uint32_t STAGE = A_BYTES + B_BYTES, TILES = ST * STAGE + CS * (C_BYTES + S_BYTES);
     static constexpr int BARS = 2 * (ST + CS) + 4;
     // at least 120 KB, so that two CTAs never share an SM's tensor memory
@@ -89,8 +94,6 @@ struct BwCfg {
     static constexpr uint32_t TMEM_COLS = 2 * BN;
     static_assert(SMEM + 512 <= 227 * 1024, "shared memory");
     static_assert(FORM != SPLIT || BN * 512u <= TILES, "a split tile's sums do not fit the rings");
-    // the groups wait on slots that their own previous stage has passed
-    static_assert(C_WARPS <= CS && GROUPS <= ST && GROUPS <= CS, "a group could run two phases ahead of a slot");
 };
 
 struct BwArgs {
@@ -100,6 +103,7 @@ struct BwArgs {
     const uint8_t* codes;       // wgrad
     const float* scales;
     const void* add;            // wgrad, may be null
+    bool add_ahead;             // its rows take bulk prefetches
     void* out;
     int64_t R, N, J, ldo;       // contraction, output rows, output columns (K)
     int bn;                     // output rows per tile (BN, or less in a pair of dgrad)
@@ -385,8 +389,24 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
         const int column = MODE == DGRAD ? (lane >> 1) + (lane & 1) * 16 : lane;      // of this tensor-memory lane
         int tile = 0;
+        // `add` is fetched into L2 a tile ahead (64 of a tile's rows of 128 values
+        // by each warp): 32 loads in flight a warp hide L2's latency, not HBM's
+        auto prefetch_add = [&](int u) {
+            if (MODE != WGRAD || !a.add_ahead || u >= units || static_cast<int64_t>(j_tile(u)) * 128 >= a.J) return;
+            const int64_t es = a.out_dt == B8_F32 ? 4 : 2;
+            for (int c = q * 32 + lane; c < bn; c += 128) {
+                const int64_t n = static_cast<int64_t>(n_tile(u)) * bn + c;
+                if (n < a.N)
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const char*>(a.add) +
+                                                                                   (n * a.ldo + static_cast<int64_t>(j_tile(u)) * 128) * es),
+                                 "r"(static_cast<uint32_t>(128 * es))
+                                 : "memory");
+            }
+        };
+        prefetch_add(u0);
         for (int u = u0; u < units; u += u_step, ++tile) {
             const int b = tile & 1;
+            prefetch_add(u + u_step);
             const int64_t j = static_cast<int64_t>(j_tile(u)) * 128 + q * 32 + column;
             const int64_t n0 = static_cast<int64_t>(n_tile(u)) * bn;
             const bool mine = FORM != PAIR || j < a.J;
@@ -672,11 +692,9 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 if (lane == 0) mbar_arrive(full_bar(qa.slot));
             }
         }
-    } else {
+    } else if (warp >= EPI_WARP0) {
         epilogue();
     }
-    if constexpr (FORM == SPLIT)
-        if (warp >= EPI_WARP0 && warp < EPI_WARP0 + EPI_WARPS) epilogue();
     __syncwarp();
     fence_before();
     if constexpr (FORM == SPLIT) {
@@ -863,6 +881,7 @@ cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M,
     a.N = M;
     a.J = K;
     a.ldo = ldw;
+    a.add_ahead = add && reinterpret_cast<uintptr_t>(add) % 16 == 0 && ldw * (dw_dt == B8_F32 ? 4 : 2) % 16 == 0;
     a.j_tiles = static_cast<int>(K / 128);
     a.out_dt = dw_dt;
     BwMaps m;

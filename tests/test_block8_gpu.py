@@ -489,6 +489,26 @@ def test_repeated_calls_give_the_same_bits():
     assert all(torch.equal(first[k], again[k]) for k in first)
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_wgrad_many_times_under_load(out):
+    """Tiles whose loads, sums and stores all compete for memory, over and over:
+    the order in which loads land changes, the bits must not."""
+    rng = np.random.default_rng(33)
+    T, M, K = 700, 6000, 4096
+    c, s = dev_codes(*codes_of(rng, T, K, 1))
+    dy = gradient(rng, T, M, torch.bfloat16)
+    base = torch.randn((M, K), device="cuda").to(out)
+    first = rb.gemm_wgrad(dy, c, s, add=base, check_device=True)
+    side = torch.cuda.Stream()
+    busy = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(20):
+        with torch.cuda.stream(side):
+            busy.fill_(i)
+        again = rb.gemm_wgrad(dy, c, s, add=base)
+        assert torch.equal(first.view(torch.uint8), again.view(torch.uint8)), i
+    torch.cuda.synchronize()
+
+
 def test_captured_and_replayed_on_new_inputs():
     case = _step_case(22)
     X, dY, bufs = case[2], case[3], case[-1]
