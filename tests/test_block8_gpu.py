@@ -373,7 +373,8 @@ def test_dgrad_output_types_and_pitches(out, pad, opad):
 
 
 @pytest.mark.parametrize("T,M,K,N,group,f16,order,name,out", [
-    (1500, 300, 4096, 2, 0, False, "sliced", "bf16", "bf16"), (1500, 1, 4096, 2, 0, True, "rows", "f16", "f32"),
+    (1500, 300, 4096, 2, 0, False, "sliced", "bf16", "bf16"), (1300, 300, 4096, 2, 0, True, "sliced", "f16", "f16"),
+    (1300, 66, 4096, 2, 128, True, "rows", "bf16", "bf16"), (600, 130, 4096, 1, 0, False, "rows", "f16", "f32"), (1500, 1, 4096, 2, 0, True, "rows", "f16", "f32"),
     (4500, 65, 1152, 1, 0, False, "rows", "f16", "f16"), (2300, 129, 2176, 3, 128, True, "sliced", "bf16", "f32"),
     (7700, 200, 640, 4, 128, False, "rows", "f16", "bf16"), (1281, 515, 4224, 2, 128, True, "sliced", "f16", "f16")])
 def test_dgrad_many_tiles(T, M, K, N, group, f16, order, name, out):
@@ -563,6 +564,42 @@ def test_check_reports_a_flag_and_the_next_call_clears_it():
         bufs[k].view(torch.int32)[1] = 2                  # what a kernel's atomicOr would leave
         assert lib.rb_gemm_check(bufs[k].data_ptr(), torch.cuda.current_stream().cuda_stream) == 6
         call()
+
+
+def test_places_past_32_bits():
+    """Rows whose byte (pack8, unpack8, wgrad) or element offsets pass 2^32."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rows, K = 33100, 65536                                   # 4.34e9 bytes of fp16
+    X = torch.empty((rows, K), dtype=torch.float16, device="cuda").normal_(generator=g)
+    c, s = rb.pack8(X)
+    ct, st = rb.pack8(X[-70:].contiguous())
+    assert torch.equal(c[-70:].view(torch.uint8), ct.view(torch.uint8)) and torch.equal(s[-70:], st)
+    cw, sw = rb.pack8(X, block_rows=128)
+    lo = (rows // 128 - 1) * 128
+    ct, st = rb.pack8(X[lo:].contiguous(), block_rows=128)
+    assert torch.equal(cw[lo:].view(torch.uint8), ct.view(torch.uint8)) and torch.equal(sw[lo // 128:], st)
+    rb.unpack8(c, s, X=X)
+    assert torch.equal(X[-70:], rb.unpack8(c[-70:], s[-70:]))
+    # the packed matrix as a weight, and as the gradient's place
+    x, xs = rb.pack8(X[:3].contiguous())
+    del X
+    y = rb.gemm8(cw, sw, x, xs)
+    h = [t.view(torch.uint8).cpu().numpy() if t.dtype == torch.float8_e4m3fn else f64(t) for t in (cw[lo:], sw[lo // 128:], x, xs)]
+    close(y[:, lo:], block8.gemm8(*h)[0], gemm8_mx_tol(*h), torch.float16)
+    del cw, sw, c, s
+    torch.cuda.empty_cache()
+    dy = torch.empty((5, 33104), dtype=torch.float16, device="cuda").normal_(generator=g)
+    dW = rb.gemm_wgrad(dy, *rb.pack8(torch.empty((5, K), dtype=torch.float16, device="cuda").normal_(generator=g)), dw_dtype=torch.float32)
+    part = dW[-8:].double()
+    assert torch.isfinite(part).all() and (part.abs().sum(1) > 0).all()
+    # row m of dW is sum_t dy[t, m] x[t]: proportional rows for proportional columns
+    dy2 = dy.clone()
+    dy2[:, :33096] = 0
+    want = rb.gemm_wgrad(dy2[:, 33096:].contiguous(), *rb.pack8(torch.ones((5, 128), dtype=torch.float16, device="cuda")))
+    del dW
+    torch.cuda.empty_cache()
+    dW = rb.gemm_wgrad(dy2, *rb.pack8(torch.ones((5, K), dtype=torch.float16, device="cuda")), dw_dtype=torch.float32)
+    assert torch.equal(dW[-8:, -128:], want) and not dW[:33096].any()
 
 
 def test_binding_refusals():
