@@ -58,6 +58,14 @@ constexpr uint32_t A_BYTES = 128 * BR * 2;      // two chunks of [64 r][64 j]
 constexpr uint32_t CHUNK = 64 * BR * 2;         // 8 KB
 enum : int { DGRAD = 0, WGRAD = 1 };
 enum : int { ONE = 0, SPLIT = 1, PAIR = 2 };
+// The tensor core cuts an accumulator's low bits off at every MMA, towards
+// zero. Of fp16 terms that leaves an error (2-norm, relative) of 1.75e-6 after
+// 2048 tokens and 1.8e-5 after 16384, where fp32 products rounded to nearest
+// stay within 1.2e-6; bf16 terms, three bits shorter, are cut less (3e-7 and
+// 6e-7 after 2048). An fp32 weight gradient is therefore summed in segments of
+// 1024 (fp16) or 2048 tokens (bf16), each added to the output so far, rounded
+// to nearest, by the epilogue; that output lies in L2 then. 16-bit outputs round far more than that away.
+constexpr int SEGMENT_F16 = 16, SEGMENT_BF16 = 32;     // stages
 // How a stage's scales (of all paths) reach shared memory:
 //   ASYNC  4-byte asynchronous copies (of fp32 values, or of pairs of fp16
 //          values that hold the wanted ones);
@@ -108,6 +116,8 @@ struct BwArgs {
     int64_t R, N, J, ldo;       // contraction, output rows, output columns (K)
     int bn;                     // output rows per tile (BN, or less in a pair of dgrad)
     int j_tiles, n_tiles;
+    bool first;                 // of the call's launches: clears the error word
+    int segment;                // stages summed in one accumulator, see SEGMENT_F16
     int out_dt;
     bool sliced, alpha_f16, g128;
     int scales_by;
@@ -342,7 +352,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     const uint32_t rank = FORM == ONE ? 0u : cluster_rank(), size = FORM == ONE ? 1u : cluster_size();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* err = a.err ? a.err : &unrecorded;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;      // flags are raised only by waits that ran out
+    if (a.first && blockIdx.x == 0 && threadIdx.x == 0) *err = 0u;      // flags are raised only by waits that ran out
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             // four expansion warps, the B loads, and in a pair's even CTA the other's word
@@ -404,9 +414,10 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             }
         };
         prefetch_add(u0);
-        for (int u = u0; u < units; u += u_step, ++tile) {
+        for (int u = u0, lo = r_lo; u < units; ++tile) {
             const int b = tile & 1;
-            prefetch_add(u + u_step);
+            const void* add = MODE != WGRAD ? nullptr : lo > r_lo ? a.out : a.add;      // a later segment: the sums so far
+            if (lo == r_lo) prefetch_add(u + u_step);
             const int64_t j = static_cast<int64_t>(j_tile(u)) * 128 + q * 32 + column;
             const int64_t n0 = static_cast<int64_t>(n_tile(u)) * bn;
             const bool mine = FORM != PAIR || j < a.J;
@@ -425,7 +436,6 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                 } else {
                     const int left = mine ? static_cast<int>(min(static_cast<int64_t>(min(32, bn - c0)), a.N - n0 - c0)) : 0;
                     const int64_t at = (n0 + c0) * a.ldo + j;
-                    const void* add = MODE == WGRAD ? a.add : nullptr;
                     if (a.out_dt == B8_F32) store_rows<float>(a.out, add, at, a.ldo, left, v);
                     else if (a.out_dt == B8_F16) store_rows<__half>(a.out, add, at, a.ldo, left, v);
                     else store_rows<__nv_bfloat16>(a.out, add, at, a.ldo, left, v);
@@ -436,6 +446,11 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             if (lane == 0) {
                 if (FORM == PAIR && rank == 1) mbar_arrive_remote(acc_empty(b), 0);
                 else mbar_arrive(acc_empty(b));
+            }
+            lo += a.segment;
+            if (lo >= r_hi) {
+                lo = r_lo;
+                u += u_step;
             }
         }
     };
@@ -586,11 +601,11 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         const uint64_t ad0 = smem_desc_mn(a_tile(0)), bd0 = MODE == DGRAD ? smem_desc(b_tile(0)) : smem_desc_mn(b_tile(0));
         // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
         constexpr uint32_t A_STEP = 128u, B_STEP = MODE == DGRAD ? 2u : 128u;
-        for (int u = u0; u < units && ok; u += u_step, ++tile) {
-            const int b = tile & 1;
+        for (int u = u0, lo = r_lo; u < units && ok; ++tile) {
+            const int b = tile & 1, hi = min(lo + a.segment, r_hi);
             const uint32_t aph = (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u, d = tmem + static_cast<uint32_t>(b * BN);
             ok = __all_sync(FULL_MASK, mbar_wait(acc_empty(b), aph, abort_flag, err, 2u));
-            for (int rb = r_lo; rb < r_hi && ok; ++rb) {
+            for (int rb = lo; rb < hi && ok; ++rb) {
                 if (!__all_sync(FULL_MASK, ready || mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u))) {
                     ok = false;
                     break;
@@ -605,18 +620,23 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
 #pragma unroll
                     for (int kk = 0; kk < BR / 16; ++kk) {
                         const uint64_t ad = ad0 + off + A_STEP * kk, bd = bd0 + off + B_STEP * kk;
-                        const uint32_t more = (rb > r_lo || kk > 0) ? 1u : 0u;
+                        const uint32_t more = (rb > lo || kk > 0) ? 1u : 0u;
                         if constexpr (FORM == PAIR) umma2_f16(d, ad, bd, idesc, more);
                         else umma_f16(d, ad, bd, idesc, more);
                     }
                     commit(empty_bar(slot));
-                    if (rb + 1 == r_hi) commit(acc_full(b));
+                    if (rb + 1 == hi) commit(acc_full(b));
                 }
                 __syncwarp();
             }
             // after an abort the teardown waits for it
             if (!ok && elect_one()) commit(acc_full(b));
             __syncwarp();
+            lo = hi;
+            if (lo >= r_hi) {
+                lo = r_lo;
+                u += u_step;
+            }
         }
         // every MMA issued has completed before the tensor memory is given up
         if (!ok)
@@ -828,6 +848,8 @@ cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, c
     BwMaps m{};
     const int bn = bwd_tile(a, true);
     plan_scales(a, NP);
+    a.segment = 1 << 30;
+    a.first = true;
     cudaError_t e = make_x_map(&m.dy, dY, a.R, a.N, ldd, bn == 256 ? a.bn / 2 : bn);
     if (e != cudaSuccess) return e;
     switch (bn) {
@@ -873,30 +895,43 @@ cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M,
                               uint32_t* err, cudaStream_t s) {
     BwArgs a{};
     a.err = err;
-    a.codes = codes;
-    a.scales = scales;
-    a.add = add;
     a.out = dW;
-    a.R = T;
     a.N = M;
     a.J = K;
     a.ldo = ldw;
-    a.add_ahead = add && reinterpret_cast<uintptr_t>(add) % 16 == 0 && ldw * (dw_dt == B8_F32 ? 4 : 2) % 16 == 0;
     a.j_tiles = static_cast<int>(K / 128);
     a.out_dt = dw_dt;
-    BwMaps m;
-    cudaError_t e = make_x_map(&m.dy, dY, M, T, ldd, BR);      // boxes of 64 m x 64 t
-    if (e == cudaSuccess) e = make_x8_map(&m.c, codes, K, T, 1, BR);
-    plan_scales(a, 1);
-    if (e != cudaSuccess) return e;
-    switch (bwd_tile(a, false)) {
-        case 32:
-        case 64: return launch_bn<WGRAD, 1, 64>(m, a, bf16, s);
-        case 128: return launch_bn<WGRAD, 1, 128>(m, a, bf16, s);
-        default: break;
+    a.R = T;
+    const int tile = bwd_tile(a, false);
+    a.n_tiles = static_cast<int>((M + (tile == 256 ? 256 : std::max(tile, 64)) - 1) / (tile == 256 ? 256 : std::max(tile, 64)));
+    // a split tile is summed in shared memory that its rings use before, so its
+    // segments are launches of their own: as many tokens as `segment` stages of each CTA
+    const int64_t nr = (static_cast<int64_t>(T) + BR - 1) / BR;
+    const int split = tile == 256 ? 1 : split_of(static_cast<int64_t>(a.j_tiles) * a.n_tiles, nr);
+    const bool fp32 = dw_dt == B8_F32;
+    const int segment = bf16 ? SEGMENT_BF16 : SEGMENT_F16;
+    const int step = fp32 && split > 1 ? std::min(T, segment * BR * split) : T;
+    a.segment = fp32 && split == 1 ? segment : 1 << 30;
+    for (int64_t t0 = 0; t0 < T; t0 += step) {
+        const int rows = static_cast<int>(std::min<int64_t>(step, T - t0));
+        a.codes = codes + t0 * K;
+        a.scales = scales + t0 * (K / 128);
+        a.add = t0 ? dW : add;
+        a.add_ahead = a.add && reinterpret_cast<uintptr_t>(a.add) % 16 == 0 && ldw * (fp32 ? 4 : 2) % 16 == 0;
+        a.R = rows;
+        a.first = t0 == 0;
+        BwMaps m;
+        // boxes of 64 m x 64 t
+        cudaError_t e = make_x_map(&m.dy, static_cast<const char*>(dY) + t0 * ldd * 2, M, rows, ldd, BR);
+        if (e == cudaSuccess) e = make_x8_map(&m.c, a.codes, K, rows, 1, BR);
+        if (e != cudaSuccess) return e;
+        plan_scales(a, 1);
+        if (tile == 256) e = bf16 ? launch<WGRAD, 1, 256, true, PAIR>(m, a, 2, s) : launch<WGRAD, 1, 256, false, PAIR>(m, a, 2, s);
+        else if (tile == 128) e = launch_bn<WGRAD, 1, 128>(m, a, bf16, s);
+        else e = launch_bn<WGRAD, 1, 64>(m, a, bf16, s);
+        if (e != cudaSuccess) return e;
     }
-    a.n_tiles = static_cast<int>((M + 255) / 256);
-    return bf16 ? launch<WGRAD, 1, 256, true, PAIR>(m, a, 2, s) : launch<WGRAD, 1, 256, false, PAIR>(m, a, 2, s);
+    return cudaSuccess;
 }
 
 }  // namespace rb

@@ -11,7 +11,9 @@ result's terms, u = 2^-24):
     ranks' sums of a split (8 u): (2^-16 + (G + 10) u) D;
     With the scales applied by the tensor cores (16-bit outputs of
     power-of-two scales) the sum of K exact products runs through: K 2^-23 D;
-  * wgrad: T products exact in fp32, `add` one more term and one more add;
+  * wgrad: T products exact in fp32, `add` one more term and one more add. An
+    fp32 output is summed in segments of 1024 or 2048 tokens (and up to 8 ranks
+    of a split): min(T, 2048) 2^-23 D and one rounded add (u) for each;
   * dgrad: the operand's rounding eps / 2 (eps of dY's type) and that of its
     scales' fp32 sum (3 u), then M products: (eps / 2 + 3 u + M 2^-23) D;
   * in these, a magnitude in D counts at least as its type's smallest normal
@@ -270,7 +272,8 @@ def check_wgrad(rng, T, M, K, name="f16", out="f32", add=None, any_scale=False, 
     # a power of two: a code of 2^-9 with a scale of 2^-16 is below fp16's 2^-24)
     x = torch.from_numpy(block8.unpack8(c, s, 1)).float().to(NAMES[name]).double().numpy()
     ref, D = block8.wgrad(f64(dy), x)[0], mags(f64(dy), name).T @ mags(x, name)
-    close(dw, ref + want_base, (T + 1) * 2.0 ** -23 * (D + np.abs(want_base)), NAMES[out])
+    n = min(T, 2048) + 1 + (T / 1024 + 8) / 2 if out == "f32" else T + 1
+    close(dw, ref + want_base, n * 2.0 ** -23 * (D + np.abs(want_base)), NAMES[out])
     return dw, base
 
 
@@ -299,8 +302,11 @@ def test_wgrad_many_tiles(T, M, K, name, out, add):
     check_wgrad(np.random.default_rng(11), T, M, K, name, out, add)
 
 
-def test_wgrad_long_sequence_few_tiles():
-    check_wgrad(np.random.default_rng(12), 20000, 72, 128, "f16")
+@pytest.mark.parametrize("T,M,K,out,add", [(20000, 72, 128, "f32", None), (40001, 72, 128, "f32", "in place"), (20000, 72, 128, "f16", "apart"),
+                                           (4500, 1300, 1024, "f32", "apart"), (2049, 1300, 1024, "f32", None), (4500, 1300, 1024, "bf16", "in place"),
+                                           (5000, 2600, 2048, "f32", "in place"), (4097, 2600, 2176, "f32", None), (2048, 2600, 2048, "f32", "apart")])
+def test_wgrad_long_sequences(T, M, K, out, add):
+    check_wgrad(np.random.default_rng(12), T, M, K, "f16" if out != "bf16" else "bf16", out, add)
 
 
 def test_wgrad_writes_only_its_columns():
