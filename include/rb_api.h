@@ -474,9 +474,12 @@ RB_API rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t
  *         X enters the product in dY's type: code * scale rounded to it, which
  *         is exact for what rb_pack8 wrote from a tensor of that type.
  * add     device, nullable, M x K values of dw_dtype with pitch ldw, added
- *         before the one rounding to dw_dtype; may be dW itself (gradients
- *         summed over micro-batches).
- * dW      device, out, [M][ldw] of dw_dtype (any rb_dtype), ldw >= K.
+ *         before the one rounding to dw_dtype; dW itself (gradients summed over
+ *         micro-batches) or apart from it.
+ * dW      device, out, [M][ldw] of dw_dtype (any rb_dtype), ldw >= K. RB_F32: the
+ *         sum is made of segments of 1024 or 2048 tokens, each added with one
+ *         rounding to nearest; what such a sum, or one with add == dW, has below
+ *         2^-126 may become zero. Others: one rounding of the fp32 sum.
  * T       1..2^22. workspace, errors: as rb_gemm8.
  */
 RB_API rb_status rb_gemm_wgrad(const void* dY, rb_dtype dy_dtype, int64_t ldd, int64_t M, const uint8_t* codes,

@@ -565,9 +565,11 @@ def gemm_wgrad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, add:
     """Weight gradient from an 8-bit checkpoint of the layer's input:
     dW = add + dY^T X with dY fp16 or bf16 [T, M] and codes, scales = pack8(X).
 
-    `add` (of dW's type and row pitch) may be dW itself: gradients summed over
-    micro-batches. The products see X rounded to dY's type (exact for a
-    checkpoint of a tensor of that type), sums are fp32 and dW is rounded once.
+    `add` (of dW's type and row pitch) is dW itself (gradients summed over
+    micro-batches) or apart from it. The products see X rounded to dY's type
+    (exact for a checkpoint of a tensor of that type); sums are fp32, and dW is
+    rounded once (fp32 dW: once for each 1024 or 2048 tokens, and sums below
+    2^-126 may become zero).
     """
     lib = _lib._lib or _lib.load()
     dev = _cuda_device(dY, codes, scales, add, dW, workspace)

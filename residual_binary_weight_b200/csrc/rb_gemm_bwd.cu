@@ -300,14 +300,23 @@ __device__ __forceinline__ void to_out(float v, float* p) { *p = v; }
 __device__ __forceinline__ void to_out(float v, __half* p) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void to_out(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
 
-// One column of up to 32 output rows (add + v), all loads before the first store.
+// One column of up to 32 output rows (add + v), all loads before the first
+// store. What is added to the fp32 output itself (a gradient summed in place, the
+// later segments) is added in L2, with nothing to wait for: 8192 tokens x
+// 14336 x 4096 from fp16 1108 -> 982 us. One thread makes all updates of an
+// element, in order, so the result does not change from run to run; sums below
+// 2^-126 become zero there.
 template <typename T>
 __device__ __forceinline__ void store_rows(void* out, const void* add, int64_t at, int64_t ldo, int left,
                                            const uint32_t (&v)[32]) {
     T* o = static_cast<T*>(out) + at;
     const T* ad = static_cast<const T*>(add) + at;
     T r[32];
-    if (left >= 32) {
+    if (sizeof(T) == 4 && left >= 32 && add == out) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(o + i * ldo), "f"(__uint_as_float(v[i])) : "memory");
+    } else if (left >= 32) {
         if (add) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) r[i] = ad[i * ldo];

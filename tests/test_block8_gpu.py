@@ -302,6 +302,20 @@ def test_wgrad_many_tiles(T, M, K, name, out, add):
     check_wgrad(np.random.default_rng(11), T, M, K, name, out, add)
 
 
+def test_wgrad_in_place_tiny_and_special_values():
+    """What is added in place keeps infinities and NaN; a sum below 2^-126 may become zero, no more."""
+    c, s = np.zeros((3, 256), np.uint8), np.ones((3, 2), np.float32)
+    dy = torch.zeros(3, 72, dtype=torch.bfloat16, device="cuda")
+    base = torch.zeros(72, 256, device="cuda")
+    special = [1e-40, -1e-40, 2.0 ** -126, float("inf"), float("-inf"), float("nan"), 1.5, -3e38]
+    base[::3, :8] = torch.tensor(special, device="cuda")
+    want = base.cpu()
+    dw = rb.gemm_wgrad(dy, *dev_codes(c, s), add=base, dW=base, check_device=True).cpu()
+    normal = (want.abs() >= 2.0 ** -126) | want.isnan()
+    assert torch.equal(dw[normal].nan_to_num(7.0), want[normal].nan_to_num(7.0))
+    assert (dw[~normal].abs() <= want[~normal].abs()).all()
+
+
 @pytest.mark.parametrize("T,M,K,out,add", [(20000, 72, 128, "f32", None), (40001, 72, 128, "f32", "in place"), (20000, 72, 128, "f16", "apart"),
                                            (4500, 1300, 1024, "f32", "apart"), (2049, 1300, 1024, "f32", None), (4500, 1300, 1024, "bf16", "in place"),
                                            (5000, 2600, 2048, "f32", "in place"), (4097, 2600, 2176, "f32", None), (2048, 2600, 2048, "f32", "apart")])
