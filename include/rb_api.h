@@ -475,7 +475,7 @@ RB_API rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t
  *         is exact for what rb_pack8 wrote from a tensor of that type.
  * add     device, nullable, M x K values of dw_dtype with pitch ldw, added
  *         before the one rounding to dw_dtype; dW itself (gradients summed over
- *         micro-batches) or apart from it.
+ *         micro-batches) or apart from it (RB_ERR_INVALID_ARG where they overlap).
  * dW      device, out, [M][ldw] of dw_dtype (any rb_dtype), ldw >= K. RB_F32: the
  *         sum is made of segments of 1024 or 2048 tokens, each added with one
  *         rounding to nearest; what such a sum, or one with add == dW, has below

@@ -573,6 +573,16 @@ static rb_status check_gradient(const void* dY, rb_dtype dy_dtype, int64_t ldd, 
     return check_header(workspace, ws_bytes);
 }
 
+// Whether two M x K matrices of one pitch (elements of es bytes, ld >= K) share
+// bytes without being the same: their rows may lie side by side.
+static bool overlap_in_part(const void* a, const void* b, int64_t M, int64_t K, int64_t ld, int64_t es) {
+    int64_t d = static_cast<int64_t>(reinterpret_cast<intptr_t>(a) - reinterpret_cast<intptr_t>(b));
+    if (d < 0) d = -d;
+    if (d == 0) return false;
+    const int64_t row = d / (ld * es), at = d % (ld * es);
+    return (row < M && at < K * es) || (row + 1 < M && ld * es - at < K * es);
+}
+
 rb_status rb_gemm_wgrad(const void* dY, rb_dtype dy_dtype, int64_t ldd, int64_t M, const uint8_t* codes,
                         const float* scales, int64_t K, int32_t T, const void* add, void* dW, rb_dtype dw_dtype,
                         int64_t ldw, void* workspace, size_t ws_bytes, void* stream) {
@@ -585,6 +595,8 @@ rb_status rb_gemm_wgrad(const void* dY, rb_dtype dy_dtype, int64_t ldd, int64_t 
     if (!aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3u))
         return fail(RB_ERR_ALIGNMENT, "codes must be 16-byte aligned, scales 4-byte aligned");
     if (reinterpret_cast<uintptr_t>(add) & (dtype8_size(dw_dtype) - 1)) return fail(RB_ERR_ALIGNMENT, "add misaligned");
+    if (add && overlap_in_part(add, dW, M, K, ldw, dtype8_size(dw_dtype)))
+        return fail(RB_ERR_INVALID_ARG, "add overlaps dW without being it");
     return launched(launch_gemm_wgrad(dY, dy_dtype == RB_BF16, ldd, M, codes, scales, K, T, add, dW, dw_dtype, ldw,
                                       error_word(workspace), static_cast<cudaStream_t>(stream)),
                     "rb_gemm_wgrad launch");

@@ -20,6 +20,13 @@
 // tiles arrive by TMA. A scale that is no power of two gets the byte 255
 // (NaN): every output that it enters is NaN, and the error word says why.
 //
+// Measured: 2048 tokens x 14336 x 4096 to bf16 111 us, 2170 TFLOP/s (94 us in
+// short bursts; under load the power cap holds the SMs near 1.3 GHz; the kernel
+// with sums in registers takes 189 us); 16 tokens x 28672 x 8192 44.7 us, 5.3 TB/s of
+// the weight's bytes (81 % of a copy's rate: the first and last loads of one wave
+// of tiles are not overlapped); one token x 4096 x 4096 8.1 us, of which HBM takes
+// 2.6 (launch, fill of the rings, sum over the cluster).
+//
 // Forms as in rb_gemm8.cu: PAIR (two accumulators of up to 224 columns, TMA
 // stores), SPLIT and ONE (128 x 128 tiles, two CTAs on each SM). Roles: the epilogue
 // warps (8 in a pair's CTA, else 4), 4 scale warps, one TMA and one MMA warp.

@@ -302,6 +302,20 @@ def test_wgrad_many_tiles(T, M, K, name, out, add):
     check_wgrad(np.random.default_rng(11), T, M, K, name, out, add)
 
 
+def test_wgrad_add_beside_dw():
+    """`add` and dW side by side in the rows of one tensor."""
+    rng = np.random.default_rng(13)
+    c, s = codes_of(rng, 65, 256, 1)
+    dy = gradient(rng, 65, 136, torch.bfloat16)
+    both = torch.from_numpy(rng.standard_normal((136, 512)).astype(np.float32)).cuda()
+    want = rb.gemm_wgrad(dy, *dev_codes(c, s), add=both[:, 256:].contiguous())
+    before = both[:, 256:].clone()
+    rb.gemm_wgrad(dy, *dev_codes(c, s), add=both[:, 256:], dW=both[:, :256])
+    assert torch.equal(both[:, :256], want) and torch.equal(both[:, 256:], before)
+    with pytest.raises(rb.RbError, match="INVALID_ARG"):
+        rb.gemm_wgrad(dy, *dev_codes(c, s), add=both[:, 128:384], dW=both[:, :256])
+
+
 def test_wgrad_in_place_tiny_and_special_values():
     """What is added in place keeps infinities and NaN; a sum below 2^-126 may become zero, no more."""
     c, s = np.zeros((3, 256), np.uint8), np.ones((3, 2), np.float32)

@@ -75,6 +75,11 @@ def test_wgrad_refusals():
     assert call(ldd=100) == call(dY=FAKE + 8) == call(codes=FAKE + 8) == call(scales=FAKE + 2) == "RB_ERR_ALIGNMENT"
     assert call(dW=FAKE + 2) == call(add=FAKE + 2) == "RB_ERR_ALIGNMENT"
     assert call(wb=0) == "RB_ERR_WORKSPACE"
+    # `add` that shares bytes with dW: half a row off, rows off, before it, in
+    # the gap between dW's rows but longer than it
+    for off in (512, 16, 1024 * 3, -1024 * 99, -4):
+        assert call(add=FAKE + off) == "RB_ERR_INVALID_ARG", off
+    assert call(ldw=400, add=FAKE + 256 * 4 - 4) == call(ldw=400, add=FAKE + 256 * 4) == "RB_ERR_INVALID_ARG"
 
 
 def test_dgrad_refusals():
