@@ -40,7 +40,7 @@
 // Measured (2048 tokens x 14336 x 4096, bf16; 1628 TFLOP/s is the measured bf16
 // peak in bursts, 1361 under the power cap, which both kernels reach, at 1.45 GHz):
 // dgrad, two paths, 197 us, 1220 TFLOP/s; wgrad without `add` 229 us, 1050
-// TFLOP/s; with an fp32 `add`, whose bytes take 36 us of HBM's time, 265 us.
+// TFLOP/s; with an fp32 `add`, whose bytes take 36 us of HBM's time, 270 us.
 // dgrad of 16 tokens through 8192 x 8192: 25 us (stage cycle, see STAGE_CYCLES);
 // wgrad of 777 tokens x 256 x 256: 8.2 us (launch, fill and the ranks' sum).
 //
