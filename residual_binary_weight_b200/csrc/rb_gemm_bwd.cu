@@ -41,7 +41,7 @@
 // peak in bursts, 1361 under the power cap, which both kernels reach, at 1.45 GHz):
 // dgrad, two paths, 197 us, 1220 TFLOP/s; wgrad without `add` 229 us, 1050
 // TFLOP/s; with an fp32 `add`, whose bytes take 36 us of HBM's time, 270 us.
-// dgrad of 16 tokens through 8192 x 8192: 25 us (stage cycle, see STAGE_CYCLES);
+// dgrad of 16 tokens through 8192 x 8192: 24.5 us (stage cycle, see STAGE_CYCLES);
 // wgrad of 777 tokens x 256 x 256: 8.2 us (launch, fill and the ranks' sum).
 //
 // Rounding: dgrad's operand W^[i][j] is the exact sum of the scales (to fp32)
@@ -91,7 +91,11 @@ struct BwCfg {
     static constexpr uint32_t S_BYTES = NP * 4 * BR;       // most bytes of a stage's scales
     // Expansion groups of four warps (a group's stage takes about 1700 cycles)
     // and copying warps.
-    static constexpr int GROUPS = 3, C_WARPS = MODE == WGRAD ? 1 : 2;
+    // A split dgrad tile of few tokens has shared memory for a fourth group and
+    // deeper rings: 16 tokens x 8192 x 8192 25.25 -> 24.5 us (six groups 24.4,
+    // but 4096 x 4096 11.14 -> 11.4, with four 11.0).
+    static constexpr bool DEEP = MODE == DGRAD && FORM == SPLIT && BN <= 64 && NP <= 2;
+    static constexpr int GROUPS = DEEP ? 4 : 3, C_WARPS = MODE == WGRAD ? 1 : 2;
     static constexpr int MMA_WARP = 0, B_WARP = 1, C_WARP = 2, EPI_WARP0 = 4, EXP_WARP0 = EPI_WARP0 + EPI_WARPS;
     static constexpr int THREADS = 32 * (EXP_WARP0 + GROUPS * GROUP_WARPS);
     // Slots are a multiple of the groups (and copying warps) that take them in
@@ -100,7 +104,7 @@ struct BwCfg {
     // slot's use while the use before, another group's, was still being
     // filled (copies land in any order), and a parity wait for the phase
     // after an open one returns at once.
-    static constexpr int ST = 6, CS = MODE == WGRAD ? 3 : 6;
+    static constexpr int ST = DEEP ? 8 : 6, CS = MODE == WGRAD ? 3 : DEEP ? 12 : 6;
     static_assert(ST % GROUPS == 0 && CS % GROUPS == 0 && CS % C_WARPS == 0, "a waiter would miss phases of its barriers");
     static constexpr uint32_t STAGE = A_BYTES + B_BYTES, TILES = ST * STAGE + CS * (C_BYTES + S_BYTES);
     static constexpr int BARS = 2 * (ST + CS) + 4;
@@ -592,16 +596,17 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     } else if (FORM == PAIR && warp == MMA_WARP && rank == 1) {
         // the pair's MMAs are issued by the even CTA: tell it, stage by stage,
         // that this CTA's half of the operands is there
-        Ring<ST> q;
-        bool ok = true;
-        for (int u = u0; u < units && ok; u += u_step) {
-            for (int rb = r_lo; rb < r_hi; ++rb, q.next()) {
-                if (!__all_sync(FULL_MASK, mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u))) {
-                    ok = false;
-                    break;
+        if (lane == 0) {
+            Ring<ST> q;
+            bool ok = true;
+            for (int u = u0; u < units && ok; u += u_step) {
+                for (int rb = r_lo; rb < r_hi; ++rb, q.next()) {
+                    if (!mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_remote(full_bar(q.slot), 0);
                 }
-                if (lane == 0) mbar_arrive_remote(full_bar(q.slot), 0);
-                __syncwarp();
             }
         }
     } else if (warp == MMA_WARP) {
@@ -617,22 +622,22 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         const uint64_t ad0 = smem_desc_mn(a_tile(0)), bd0 = MODE == DGRAD ? smem_desc(b_tile(0)) : smem_desc_mn(b_tile(0));
         // 16 rows r on: two 1024-byte atoms (M- or N-major), 32 bytes (K-major)
         constexpr uint32_t A_STEP = 128u, B_STEP = MODE == DGRAD ? 2u : 128u;
-        for (int u = u0, lo = r_lo; u < units && ok; ++tile) {
-            const int b = tile & 1, hi = min(lo + a.segment, r_hi);
-            const uint32_t aph = (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u, d = tmem + static_cast<uint32_t>(b * BN);
-            ok = __all_sync(FULL_MASK, mbar_wait(acc_empty(b), aph, abort_flag, err, 2u));
-            for (int rb = lo; rb < hi && ok; ++rb) {
-                if (!__all_sync(FULL_MASK, ready || mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u))) {
-                    ok = false;
-                    break;
-                }
-                const int slot = q.slot;
-                q.next();
-                // the next stage's barrier is looked at while this one's MMAs are issued
-                ready = mbar_test(full_bar(q.slot), q.ph);
-                fence_after();
-                const uint32_t off = static_cast<uint32_t>(slot) * (C::STAGE >> 4);
-                if (elect_one()) {
+        // One lane runs the loop: with a stage's votes, election and
+        // reconvergence a warp was 1 to 3 % slower (dgrad, 64 tokens x 8192 x
+        // 8192 28.2 -> 27.4 us).
+        if (elect_one()) {
+            for (int u = u0, lo = r_lo; u < units && ok; ++tile) {
+                const int b = tile & 1, hi = min(lo + a.segment, r_hi);
+                const uint32_t aph = (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u, d = tmem + static_cast<uint32_t>(b * BN);
+                ok = mbar_wait(acc_empty(b), aph, abort_flag, err, 2u);
+                for (int rb = lo; rb < hi && ok; ++rb) {
+                    if (!ready && !mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const int slot = q.slot;
+                    const uint32_t off = static_cast<uint32_t>(slot) * (C::STAGE >> 4);
 #pragma unroll
                     for (int kk = 0; kk < BR / 16; ++kk) {
                         const uint64_t ad = ad0 + off + A_STEP * kk, bd = bd0 + off + B_STEP * kk;
@@ -642,21 +647,22 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                     }
                     commit(empty_bar(slot));
                     if (rb + 1 == hi) commit(acc_full(b));
+                    q.next();
+                    ready = mbar_test(full_bar(q.slot), q.ph);
                 }
-                __syncwarp();
+                // after an abort the teardown waits for it
+                if (!ok) commit(acc_full(b));
+                lo = hi;
+                if (lo >= r_hi) {
+                    lo = r_lo;
+                    u += u_step;
+                }
             }
-            // after an abort the teardown waits for it
-            if (!ok && elect_one()) commit(acc_full(b));
-            __syncwarp();
-            lo = hi;
-            if (lo >= r_hi) {
-                lo = r_lo;
-                u += u_step;
-            }
+            // every MMA issued has completed before the tensor memory is given up
+            if (!ok)
+                for (int i = tile - 1; i >= 0 && i >= tile - 2; --i)
+                    mbar_drain(acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u);
         }
-        // every MMA issued has completed before the tensor memory is given up
-        if (!ok)
-            for (int i = tile - 1; i >= 0 && i >= tile - 2; --i) mbar_drain(acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u);
     } else if (warp >= EXP_WARP0) {
         // A thread expands two rows of a stage, 32 columns of each. wgrad: warp wq
         // takes columns 32 wq.. of rows lane and lane + 32. dgrad: 4 lanes
@@ -802,7 +808,7 @@ cudaError_t launch(const BwMaps& m, BwArgs& a, int cluster, cudaStream_t s) {
 }
 
 // A stage takes about 600 cycles (the MMA warp's waits, issue and commit; the
-// expansion: 1700 cycles of each of three groups) or its MMAs' 2 bn in a pair, whichever is more. Time in stages of
+// expansion: 1700 cycles of each group) or its MMAs' 2 bn in a pair, whichever is more. Time in stages of
 // the two ways to cover N rows of dY of more than 64:
 constexpr int64_t STAGE_CYCLES = 600;
 
