@@ -302,6 +302,31 @@ def test_wgrad_many_tiles(T, M, K, name, out, add):
     check_wgrad(np.random.default_rng(11), T, M, K, name, out, add)
 
 
+@pytest.mark.parametrize("T,M,K", [(9000, 72, 128), (2500, 2600, 2048)])
+def test_wgrad_in_place_replayed(T, M, K):
+    """A captured in-place gradient of several segments, replayed: each replay
+    adds the same again, as eager calls do, on another stream than the capture's."""
+    rng = np.random.default_rng(14)
+    c, s = dev_codes(*codes_of(rng, T, K, 1))
+    dy = gradient(rng, T, M, torch.float16)
+    base = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).cuda()
+    eager, dw = base.clone(), base.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rb.gemm_wgrad(dy, c, s, add=dw, dW=dw)
+    assert torch.equal(dw, base)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            graph.replay()
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        rb.gemm_wgrad(dy, c, s, add=eager, dW=eager, check_device=True)
+    assert torch.equal(dw, eager)
+
+
 def test_wgrad_add_beside_dw():
     """`add` and dW side by side in the rows of one tensor."""
     rng = np.random.default_rng(13)
