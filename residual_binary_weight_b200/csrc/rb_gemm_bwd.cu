@@ -299,12 +299,13 @@ __device__ __forceinline__ void store_out(void* p, int dt, int64_t i, float v) {
     else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// asynchronous copies global -> shared; `in` false: zeros
+// asynchronous copies global -> shared; cp_async4 reads the first `bytes` of 4 and
+// fills the rest with zeros
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void to_out(float v, float* p) { *p = v; }
@@ -554,14 +555,18 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                         const char* src = in ? sp + 32 * k * s_row : scales;
 #pragma unroll
                         for (int p = 0; p < NP; ++p)
-                            cp_async4(s_tile(q.slot) + p * a.scale_path + (lane + 32 * k) * 4u, src + (in ? p * s_path : 0), in);
+                            cp_async4(s_tile(q.slot) + p * a.scale_path + (lane + 32 * k) * 4u, src + (in ? p * s_path : 0), in ? 4u : 0u);
                     }
                 }
                 if (MODE == DGRAD && pairs) {
                     const char* src = left > 0 ? sp : scales;               // rows 2 lane and 2 lane + 1
+                    // of an odd number of rows, the last has nothing after it: what lies there
+                    // is not the array's, and as a scale of row M it would turn dY's
+                    // zeros into NaN if it were infinite
+                    const uint32_t bytes = left > 1 ? 4u : left > 0 ? 2u : 0u;
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
-                        cp_async4(s_tile(q.slot) + p * a.scale_path + lane * 4u, src + (left > 0 ? p * s_path : 0), left > 0);
+                        cp_async4(s_tile(q.slot) + p * a.scale_path + lane * 4u, src + (left > 0 ? p * s_path : 0), bytes);
                 }
                 if (MODE == DGRAD && loaded) {
                     asm volatile("cp.async.wait_all;" ::: "memory");

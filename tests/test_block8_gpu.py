@@ -440,6 +440,28 @@ def test_dgrad_many_tiles(T, M, K, N, group, f16, order, name, out):
     check_dgrad(np.random.default_rng(15), T, M, K, N, group, f16, order, name, out)
 
 
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("order", ["rows", "sliced"])
+@pytest.mark.parametrize("T,M,K", [(1, 1, 128), (5, 65, 640), (70, 515, 1024), (300, 333, 384),     # split tiles
+                                   (20, 65, 9856), (40, 1, 9728), (70, 333, 9728),                  # one tile a CTA
+                                   (1500, 65, 4096), (1300, 515, 4096)])                             # pairs
+def test_dgrad_fp16_scales_of_an_odd_number_of_rows(T, M, K, order, name):
+    """One path, a scale per row: what lies after the last scale stays out of the result."""
+    rng = np.random.default_rng(T + M)
+    planes, a = plane_case(rng, M, K, 1, 0, True)
+    buf = torch.full((M + 129,), float("nan"), dtype=torch.float16, device="cuda")
+    buf[:M] = torch.from_numpy(a).cuda().view(-1)
+    dy = gradient(rng, T, M, NAMES[name])
+    p = rows_to_sliced(planes) if order == "sliced" else planes
+    dx = rb.gemm_dgrad(torch.from_numpy(p.view(np.int32)).cuda(), buf[:M].view(1, M, 1), dy, K, dx_dtype=NAMES[name],
+                       check_device=True)
+    ref, D = block8.dgrad(f64(dy), planes, a.astype(np.float64))
+    eps = torch.finfo(NAMES[name]).eps
+    tiny = torch.finfo(NAMES[name]).smallest_normal * eps / 2
+    Dm = mags(f64(dy), name) @ mags(block8.weight(planes, a), name)
+    close(dx, ref, eps / 2 * D + M * 2.0 ** -23 * Dm + tiny * np.abs(f64(dy)).sum(1, keepdims=True), NAMES[name])
+
+
 def test_dgrad_agrees_with_differences_of_the_forward():
     """<C, gemm(x + e) - gemm(x - e)> / 2 against <dX, e>: the forward is linear
     in x (planes fixed), so the difference is the derivative but for both
