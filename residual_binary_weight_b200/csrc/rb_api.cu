@@ -47,15 +47,13 @@ int device_sm_count() {
     return cache[dev];
 }
 
-cudaError_t allow_smem(const void* kernel, size_t bytes, SmemMark& mark) {
+cudaError_t allow_smem(const void* kernel, size_t bytes, SmemLimit& limit) {
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const bool known = dev >= 0 && dev < SmemMark::DEVICES;
-    if (known && mark.bytes[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e == cudaSuccess && known) mark.bytes[dev].store(static_cast<uint32_t>(bytes), std::memory_order_release);
-    return e;
+    return limit.raise(dev, bytes, [&](size_t b) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(b));
+    });
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

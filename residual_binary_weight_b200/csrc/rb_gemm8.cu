@@ -481,8 +481,8 @@ template <int FORM>
 cudaError_t launch(const CUtensorMap& xm, const CUtensorMap& wm, const CUtensorMap& ym, const G8Args& a, unsigned grid,
                    unsigned cluster, size_t smem, cudaStream_t s) {
     auto kern = gemm8_kernel<FORM>;
-    static SmemMark mark;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, mark);
+    static SmemLimit limit;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, limit);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);

@@ -792,8 +792,8 @@ template <int MODE, int NP, int BN, bool BF16, int FORM>
 cudaError_t launch(const BwMaps& m, BwArgs& a, int cluster, cudaStream_t s) {
     constexpr size_t smem = BwCfg<MODE, NP, BN, FORM>::SMEM;
     auto kern = gemm_bwd_kernel<MODE, NP, BN, BF16, FORM>;
-    static SmemMark mark;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, mark);
+    static SmemLimit limit;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, limit);
     if (e != cudaSuccess) return e;
     const int64_t units = static_cast<int64_t>(FORM == PAIR ? (a.j_tiles + 1) / 2 : a.j_tiles) * a.n_tiles;
     const int64_t sms = device_sm_count();

@@ -5,7 +5,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
-#include <atomic>
+#include "rb_smem.h"
 
 namespace rb {
 
@@ -155,14 +155,10 @@ cudaError_t launch_gemm_dgrad(const uint32_t* planes, const void* alpha, bool al
 
 int device_sm_count();
 
-// Lets `kernel` use `bytes` of dynamic shared memory on the current device. The
-// mark, one per kernel, remembers it: the runtime call costs more than all
-// other checks of a small launch. (Two threads may both make the call.)
-struct SmemMark {
-    static constexpr int DEVICES = 64;
-    std::atomic<uint32_t> bytes[DEVICES] = {};
-};
-cudaError_t allow_smem(const void* kernel, size_t bytes, SmemMark& mark);
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device, now
+// and in later calls. `limit`, one per kernel, remembers it: the runtime call
+// costs more than all other checks of a small launch.
+cudaError_t allow_smem(const void* kernel, size_t bytes, SmemLimit& limit);
 
 // Device address of the static scratch array of rb_gemv_noalloc on the
 // current device (looked up once per device).

@@ -25,6 +25,10 @@ result's terms, u = 2^-24):
   * the output's rounding eps / 2 of the value, and half of the smallest
     subnormal.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -632,6 +636,46 @@ def test_two_streams_at_once():
     for c, w in zip(cases, want):
         got = _bits(c[-1])
         assert all(torch.equal(w[k], got[k]) for k in w)
+
+
+FIRST_CALLS = """
+import threading
+import torch
+import residual_binary_weight_b200 as rb
+
+g = torch.Generator(device="cuda").manual_seed(7)
+# kernels whose shared memory depends on the number of tokens: both scale forms, split and whole tiles
+Ts, shapes = (1, 128, 16, 100, 3, 33), ((256, 512), (20000, 128))
+W = {s: rb.pack8(torch.randn(s, generator=g, device="cuda"), block_rows=128) for s in shapes}
+X = {(T, s): rb.pack8(torch.randn((T, s[1]), generator=g, device="cuda")) for T in Ts for s in shapes}
+torch.cuda.synchronize()
+gate, out, failed = threading.Barrier(len(Ts)), {}, []
+
+def work(T):
+    try:
+        for s in shapes:
+            for pow2 in (True, False):
+                gate.wait()
+                out[T, s, pow2] = rb.gemm8(*W[s], *X[T, s], pow2_scales=pow2, check_device=True)
+    except Exception as e:
+        failed.append((T, e))
+        gate.abort()
+
+threads = [threading.Thread(target=work, args=(T,)) for T in Ts]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert not failed, failed
+for (T, s, pow2), y in out.items():
+    assert torch.equal(rb.gemm8(*W[s], *X[T, s], pow2_scales=pow2, check_device=True), y), (T, s, pow2)
+print("ok")
+"""
+
+
+def test_first_calls_of_several_threads():
+    """A fresh process whose threads make the first calls at once, with different needs of shared memory."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "ok", (out.returncode, out.stdout, out.stderr)
 
 
 def test_check_reports_a_flag_and_the_next_call_clears_it():
