@@ -479,7 +479,9 @@ RB_API rb_status rb_gemm8(const uint8_t* w, const float* w_scales, const uint8_t
  * dW      device, out, [M][ldw] of dw_dtype (any rb_dtype), ldw >= K. RB_F32: the
  *         sum is made of segments of 1024 or 2048 tokens, each added with one
  *         rounding to nearest; what such a sum, or one with add == dW, has below
- *         2^-126 may become zero. Others: one rounding of the fp32 sum.
+ *         2^-126 may become zero. Others: one rounding of the sum of dY^T X and add.
+ *         Within a segment (16384 tokens for 16-bit dW) the tensor cores sum, and
+ *         cut low bits off towards zero: up to about 6e-9 of the terms' magnitudes a token.
  * T       1..2^22. workspace, errors: as rb_gemm8.
  */
 RB_API rb_status rb_gemm_wgrad(const void* dY, rb_dtype dy_dtype, int64_t ldd, int64_t M, const uint8_t* codes,
@@ -492,8 +494,10 @@ RB_API rb_status rb_gemm_wgrad(const void* dY, rb_dtype dy_dtype, int64_t ldd, i
  * straight from the sign planes: neither W^ nor its transpose is stored.
  * W^[i][j] (the sum of the fp32 values of its scales) is rounded once to dY's
  * type, so a result is within eps / 2 * sum_i |dY[t][i] W^[i][j]| (eps / 2 =
- * 2^-11 for fp16, 2^-8 for bf16) of the unrounded product, plus fp32 sums and
- * the rounding to dx_dtype.
+ * 2^-11 for fp16, 2^-8 for bf16) of the unrounded product, plus the sums' error and
+ * the rounding to dx_dtype. Sums are made of segments of 1024 (fp16 dY) or 2048 rows
+ * (bf16) for fp32 dX and of 16384 rows for 16-bit dX, each added with one rounding
+ * to nearest; within a segment as in rb_gemm_wgrad.
  *
  * planes, alpha, alpha_dtype, L  as rb_gemm; 1..4 paths; scales RB_F32 or
  *         RB_F16 in either grouping.

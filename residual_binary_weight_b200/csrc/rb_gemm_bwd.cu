@@ -66,13 +66,19 @@ constexpr uint32_t CHUNK = 64 * BR * 2;         // 8 KB
 enum : int { DGRAD = 0, WGRAD = 1 };
 enum : int { ONE = 0, SPLIT = 1, PAIR = 2 };
 // The tensor core cuts an accumulator's low bits off at every MMA, towards
-// zero. Of fp16 terms that leaves an error (2-norm, relative) of 1.75e-6 after
-// 2048 tokens and 1.8e-5 after 16384, where fp32 products rounded to nearest
-// stay within 1.2e-6; bf16 terms, three bits shorter, are cut less (3e-7 and
-// 6e-7 after 2048). An fp32 weight gradient is therefore summed in segments of
-// 1024 (fp16) or 2048 tokens (bf16), each added to the output so far, rounded
-// to nearest, by the epilogue; that output lies in L2 then. 16-bit outputs round far more than that away.
-constexpr int SEGMENT_F16 = 16, SEGMENT_BF16 = 32;     // stages
+// zero, so the error grows with the number of terms: of fp16 terms of one sign
+// it is 5.4e-6 of the sum after 1024 terms, 9.6e-5 after 16384 and 1.5e-3 after 262144
+// (bf16: 1.3e-6, 6.7e-5, 1.5e-3), of random signs 1.0e-6, 1.8e-5 and 3e-4 (2-norm).
+// A long contraction is therefore summed in segments, each from an accumulator
+// of its own, added to the sum so far with one rounding to nearest by the epilogue:
+// fp32 outputs in segments of 1024 (fp16) or 2048 terms (bf16), 16-bit outputs
+// of 16384, whose 1e-4 is a fifth of fp16's half step.
+// The sum so far stays in tensor memory (2048 tokens x 14336 x 4096 to fp32 dX from
+// bf16 201 -> 213 us, from fp16 210 -> 248 us: a pair's tile leaves room for one
+// accumulator beside it, so its MMAs wait for the epilogue at a segment's end). Of an fp32
+// weight gradient it is the output itself, which lies in L2 then, and a split
+// one takes a launch for each segment.
+constexpr int SEGMENT_F16 = 16, SEGMENT_BF16 = 32, SEGMENT_OUT16 = 256;     // stages
 // How a stage's scales (of all paths) reach shared memory:
 //   ASYNC  4-byte asynchronous copies (of fp32 values, or of pairs of fp16
 //          values that hold the wanted ones);
@@ -110,7 +116,10 @@ struct BwCfg {
     static constexpr int BARS = 2 * (ST + CS) + 4;
     // at least 120 KB, so that two CTAs never share an SM's tensor memory
     static constexpr uint32_t SMEM = (TILES < 119u * 1024u ? 119u * 1024u : TILES) + 1024u;
-    static constexpr uint32_t TMEM_COLS = 2 * BN;
+    // two accumulators and, from column SUM_COL on, a sum of segments (in a
+    // pair in the place of the second accumulator)
+    static constexpr uint32_t TMEM_COLS = 2 * BN, SUM_COL = FORM == PAIR ? BN : 2 * BN, SUM_TMEM_COLS = FORM == PAIR ? 2 * BN : 4 * BN;
+    static_assert(SUM_TMEM_COLS <= 512, "tensor memory");
     static_assert(SMEM + 512 <= 227 * 1024, "shared memory");
     static_assert(FORM != SPLIT || BN * 512u <= TILES, "a split tile's sums do not fit the rings");
 };
@@ -129,6 +138,7 @@ struct BwArgs {
     int j_tiles, n_tiles;
     bool first;                 // of the call's launches: clears the error word
     int segment;                // stages summed in one accumulator, see SEGMENT_F16
+    bool sum_in_tmem;           // where the segments before are summed: tensor memory, or the output
     int out_dt;
     bool sliced, alpha_f16, g128;
     int scales_by;
@@ -392,9 +402,10 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         abort_word = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    const uint32_t tmem_cols = a.sum_in_tmem ? C::SUM_TMEM_COLS : C::TMEM_COLS;
     if (warp == MMA_WARP) {
-        if constexpr (FORM == PAIR) tmem_alloc2(smem_addr(&tmem_slot), C::TMEM_COLS);
-        else tmem_alloc(smem_addr(&tmem_slot), C::TMEM_COLS);
+        if constexpr (FORM == PAIR) tmem_alloc2(smem_addr(&tmem_slot), tmem_cols);
+        else tmem_alloc(smem_addr(&tmem_slot), tmem_cols);
     }
     fence_before();
     if constexpr (FORM == PAIR) cluster_sync();      // the peer's barriers are ready, too
@@ -414,6 +425,8 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     const int u_step = FORM == SPLIT ? units : static_cast<int>(gridDim.x / size);
     auto j_tile = [&](int u) { return FORM == PAIR ? 2 * (u % jw) + static_cast<int>(rank) : u % jw; };
     auto n_tile = [&](int u) { return u / jw; };
+    // accumulators in turn: two, but one where a pair's other one holds the sum
+    const int flip = FORM == PAIR && a.sum_in_tmem ? 0 : 1;
 
     auto epilogue = [&] {
         const int q = warp - EPI_WARP0;          // lane quarter
@@ -436,18 +449,36 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         };
         prefetch_add(u0);
         for (int u = u0, lo = r_lo; u < units; ++tile) {
-            const int b = tile & 1;
-            const void* add = MODE != WGRAD ? nullptr : lo > r_lo ? a.out : a.add;      // a later segment: the sums so far
+            const int b = tile & flip;
+            const bool keep = a.sum_in_tmem && lo + a.segment < r_hi;
+            // to a later segment, the sums so far
+            const void* add = MODE != WGRAD ? nullptr : lo > r_lo && !a.sum_in_tmem ? a.out : a.add;
             if (lo == r_lo) prefetch_add(u + u_step);
             const int64_t j = static_cast<int64_t>(j_tile(u)) * 128 + q * 32 + column;
             const int64_t n0 = static_cast<int64_t>(n_tile(u)) * bn;
             const bool mine = FORM != PAIR || j < a.J;
-            if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(tile >> 1) & 1u, abort_flag, err, 8u)) ||
+            if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), static_cast<uint32_t>(tile >> flip) & 1u, abort_flag, err, 8u)) ||
                 *abort_flag)
                 break;
             fence_after();
+            // a segment joins the sum so far: there, or the last one in its accumulator
+            if (a.sum_in_tmem) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < bn; c0 += 32) {
+                for (int c0 = 0; c0 < bn; c0 += 16) {
+                    const uint32_t acc = tmem + lanes + static_cast<uint32_t>(b * BN + c0), sum = tmem + lanes + C::SUM_COL + static_cast<uint32_t>(c0);
+                    uint32_t v[16], w[16];
+                    tmem_load<16>(acc, v);
+                    if (lo > r_lo) {
+                        tmem_load<16>(sum, w);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+                    }
+                    tmem_store16(keep ? sum : acc, v);
+                }
+                tmem_store_wait();
+            }
+#pragma unroll 1
+            for (int c0 = 0; c0 < bn && !keep; c0 += 32) {
                 uint32_t v[32];
                 tmem_load<32>(tmem + lanes + static_cast<uint32_t>(b * BN + c0), v);
                 if constexpr (FORM == SPLIT) {
@@ -526,7 +557,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         for (int u = u0; u < units && ok; u += u_step, it = (it + r_hi - r_lo) % C_WARPS) {
             const int jt = min(j_tile(u), a.j_tiles - 1);
             int rb = r_lo + (mine - it + C_WARPS) % C_WARPS;
-            int64_t left = a.R - (static_cast<int64_t>(rb) * BR + (pairs ? 2 * lane : lane));     // rows from this lane's first
+            int left = static_cast<int>(a.R - (static_cast<int64_t>(rb) * BR + (pairs ? 2 * lane : lane)));     // rows from this lane's first
             const char* wp = planes + (a.sliced ? static_cast<int64_t>(jt >> 2) * a.R * 64 + (jt & 3) * 16 : static_cast<int64_t>(jt) * 16) +
                              (static_cast<int64_t>(rb) * BR + lane) * w_row;
             const char* sp = scales + (per_block ? (static_cast<int64_t>(jt) * es & (loaded ? ~1ll : ~3ll)) : 0) +
@@ -540,7 +571,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                     mbar_arrive_expect_tx(full_c(q.slot), C::C_BYTES);
                     tma_load_3d(c_tile(q.slot), &cmap, j_tile(u) * 128, rb * BR, 0, full_c(q.slot));
                 }
-                const int64_t rows_left = pairs ? left + lane : left;      // from row lane of the stage
+                const int rows_left = pairs ? left + lane : left;      // from row lane of the stage
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if constexpr (MODE == DGRAD) {
@@ -563,7 +594,7 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
                     // of an odd number of rows, the last has nothing after it: what lies there
                     // is not the array's, and as a scale of row M it would turn dY's
                     // zeros into NaN if it were infinite
-                    const uint32_t bytes = left > 1 ? 4u : left > 0 ? 2u : 0u;
+                    const uint32_t bytes = static_cast<uint32_t>(2 * max(min(left, 2), 0));
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
                         cp_async4(s_tile(q.slot) + p * a.scale_path + lane * 4u, src + (left > 0 ? p * s_path : 0), bytes);
@@ -632,8 +663,8 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
         // 8192 28.2 -> 27.4 us).
         if (elect_one()) {
             for (int u = u0, lo = r_lo; u < units && ok; ++tile) {
-                const int b = tile & 1, hi = min(lo + a.segment, r_hi);
-                const uint32_t aph = (static_cast<uint32_t>(tile >> 1) & 1u) ^ 1u, d = tmem + static_cast<uint32_t>(b * BN);
+                const int b = tile & flip, hi = min(lo + a.segment, r_hi);
+                const uint32_t aph = (static_cast<uint32_t>(tile >> flip) & 1u) ^ 1u, d = tmem + static_cast<uint32_t>(b * BN);
                 ok = mbar_wait(acc_empty(b), aph, abort_flag, err, 2u);
                 for (int rb = lo; rb < hi && ok; ++rb) {
                     if (!ready && !mbar_wait(full_bar(q.slot), q.ph, abort_flag, err, 2u)) {
@@ -665,8 +696,8 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
             }
             // every MMA issued has completed before the tensor memory is given up
             if (!ok)
-                for (int i = tile - 1; i >= 0 && i >= tile - 2; --i)
-                    mbar_drain(acc_full(i & 1), static_cast<uint32_t>(i >> 1) & 1u);
+                for (int i = tile - 1; i >= 0 && i >= tile - 1 - flip; --i)
+                    mbar_drain(acc_full(i & flip), static_cast<uint32_t>(i >> flip) & 1u);
         }
     } else if (warp >= EXP_WARP0) {
         // A thread expands two rows of a stage, 32 columns of each. wgrad: warp wq
@@ -767,8 +798,8 @@ gemm_bwd_kernel(const __grid_constant__ CUtensorMap dmap, const __grid_constant_
     }
     fence_after();
     if (warp == MMA_WARP) {
-        if constexpr (FORM == PAIR) tmem_dealloc2(tmem, C::TMEM_COLS);
-        else tmem_dealloc(tmem, C::TMEM_COLS);
+        if constexpr (FORM == PAIR) tmem_dealloc2(tmem, tmem_cols);
+        else tmem_dealloc(tmem, tmem_cols);
     }
 }
 
@@ -797,6 +828,13 @@ cudaError_t launch(const BwMaps& m, BwArgs& a, int cluster, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int64_t units = static_cast<int64_t>(FORM == PAIR ? (a.j_tiles + 1) / 2 : a.j_tiles) * a.n_tiles;
     const int64_t sms = device_sm_count();
+    // segments, where a CTA has more stages than one holds (launch_gemm_wgrad
+    // sees to it that a split fp32 weight gradient has not)
+    const bool fp32 = a.out_dt == B8_F32;
+    const int64_t ctas = FORM == SPLIT ? cluster : 1, stages = ((a.R + BR - 1) / BR + ctas - 1) / ctas;
+    const int segment = !fp32 ? SEGMENT_OUT16 : BF16 ? SEGMENT_BF16 : SEGMENT_F16;
+    a.segment = stages > segment ? segment : 1 << 30;
+    a.sum_in_tmem = stages > segment && (MODE == DGRAD || !fp32);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(FORM == SPLIT ? units * cluster : FORM == PAIR ? 2 * std::min(units, sms / 2)
                                                                                              : std::min(units, sms)));
@@ -875,7 +913,6 @@ cudaError_t launch_dgrad_np(BwArgs& a, const void* dY, int64_t ldd, bool bf16, c
     BwMaps m{};
     const int bn = bwd_tile(a, true);
     plan_scales(a, NP);
-    a.segment = 1 << 30;
     a.first = true;
     cudaError_t e = make_x_map(&m.dy, dY, a.R, a.N, ldd, bn == 256 ? a.bn / 2 : bn);
     if (e != cudaSuccess) return e;
@@ -936,9 +973,7 @@ cudaError_t launch_gemm_wgrad(const void* dY, bool bf16, int64_t ldd, int64_t M,
     const int64_t nr = (static_cast<int64_t>(T) + BR - 1) / BR;
     const int split = tile == 256 ? 1 : split_of(static_cast<int64_t>(a.j_tiles) * a.n_tiles, nr);
     const bool fp32 = dw_dt == B8_F32;
-    const int segment = bf16 ? SEGMENT_BF16 : SEGMENT_F16;
-    const int step = fp32 && split > 1 ? std::min(T, segment * BR * split) : T;
-    a.segment = fp32 && split == 1 ? segment : 1 << 30;
+    const int step = fp32 && split > 1 ? std::min(T, (bf16 ? SEGMENT_BF16 : SEGMENT_F16) * BR * split) : T;
     for (int64_t t0 = 0; t0 < T; t0 += step) {
         const int rows = static_cast<int>(std::min<int64_t>(step, T - t0));
         a.codes = codes + t0 * K;

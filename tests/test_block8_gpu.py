@@ -466,6 +466,73 @@ def test_dgrad_fp16_scales_of_an_odd_number_of_rows(T, M, K, order, name):
     close(dx, ref, eps / 2 * D + M * 2.0 ** -23 * Dm + tiny * np.abs(f64(dy)).sum(1, keepdims=True), NAMES[name])
 
 
+@pytest.mark.parametrize("T,M,K,N,group,f16,order,name,out", [
+    (5, 20000, 640, 2, 0, False, "rows", "f16", "f32"), (70, 20000, 1024, 1, 128, True, "sliced", "bf16", "f32"),      # split tiles
+    (5, 140000, 128, 2, 0, True, "sliced", "f16", "f16"), (100, 140000, 128, 1, 0, False, "rows", "bf16", "bf16"),
+    (20, 3000, 9856, 2, 0, False, "sliced", "f16", "f32"), (1100, 16600, 1152, 2, 0, False, "rows", "bf16", "f16"),    # one tile a CTA
+    (600, 3000, 4096, 2, 0, False, "sliced", "f16", "f32"), (1300, 4500, 2176, 4, 128, True, "rows", "bf16", "f32"),   # pairs
+    (1300, 16600, 2176, 1, 0, True, "rows", "f16", "f16")])
+def test_dgrad_of_many_rows(T, M, K, N, group, f16, order, name, out):
+    """More rows than one accumulator sums, in every form."""
+    check_dgrad(np.random.default_rng(19), T, M, K, N, group, f16, order, name, out)
+
+
+def summed_of_one_sign(got, terms, dt, split_sums=8):
+    """Against the fp64 sum of `terms` [.., n] of one sign, the worst case of an
+    accumulator that truncates: a segment of S terms is within S 2^-23 of its sum
+    (S = 1024 of fp16 and 2048 of bf16 terms for fp32 results, 16384 for 16-bit ones),
+    segments and a split's ranks are added with one rounding each."""
+    S = 16384 if got.dtype != torch.float32 else 1024 if dt == torch.float16 else 2048
+    n = terms.shape[-1]
+    ref = terms.double().sum(-1, keepdim=True)
+    tol = (S * 2.0 ** -23 + (n / S + split_sums) * U) * ref
+    err = (got.double() - ref).abs()
+    lim = tol + torch.finfo(got.dtype).eps / 2 * (ref + tol)
+    assert (err <= lim).all(), float((err / ref).max())
+
+
+@pytest.mark.parametrize("name,out", [("f16", "f32"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("T,M,K", [(2, 20, 128), (16, 17, 9728), (600, 17, 4096)])      # split, one, pairs
+def test_dgrad_long_sums_of_one_sign(T, M, K, name, out):
+    M = 1 << (M if out == "f32" else 23 if M == 20 else 20)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dt = NAMES[name]
+    planes = torch.full((1, M, K // 32), -1, dtype=torch.int32, device="cuda")
+    alpha = ((torch.rand((1, M, 1), generator=g, device="cuda") + 0.5) * 2.0 ** -7).bfloat16().half()      # exact in both types
+    dy = ((torch.rand((T, M), generator=g, device="cuda") + 1) * 2.0 ** -11).to(dt)
+    dx = rb.gemm_dgrad(planes, alpha, dy, K, dx_dtype=NAMES[out], check_device=True)
+    assert torch.equal(dx, dx[:, :1].expand(-1, K))
+    for t in range(0, T, 37):
+        summed_of_one_sign(dx[t, :1], dy[t].double() * alpha.double().view(-1), dt)
+
+
+@pytest.mark.parametrize("name,out", [("f16", "f16"), ("bf16", "f16")])
+@pytest.mark.parametrize("T,M,K", [(22, 64, 128), (20, 2600, 2048)])      # split, pairs
+def test_wgrad_long_sums_of_one_sign(T, M, K, name, out):
+    T = 1 << T
+    g = torch.Generator(device="cuda").manual_seed(10)
+    dt = NAMES[name]
+    dy = torch.empty((T, M), dtype=dt, device="cuda")
+    x = torch.empty((T, K), dtype=torch.float16, device="cuda")
+    # one column of values each, so that one fp64 sum is the reference of all results
+    dy[:] = ((torch.rand((T, 1), generator=g, device="cuda") + 1) * 2.0 ** -11).to(dt)
+    x[:] = ((torch.rand((T, 1), generator=g, device="cuda") + 1) * 2.0 ** -6).to(torch.float16)
+    c, s = rb.pack8(x)
+    x1 = rb.unpack8(c[:, :128].contiguous(), s[:, :1].contiguous())[:, 0]
+    del x
+    dw = rb.gemm_wgrad(dy, c, s, dw_dtype=NAMES[out], check_device=True)
+    assert torch.equal(dw, dw[:1, :1].expand(M, K))
+    summed_of_one_sign(dw[0, :1], dy[:, 0].double() * x1.double(), dt)
+
+
+@pytest.mark.parametrize("T,M,K,name,out,add", [(140000, 72, 128, "f16", "f16", "in place"), (140000, 40, 256, "bf16", "bf16", None),
+                                                (16600, 1100, 1152, "bf16", "bf16", "apart"), (16600, 1300, 2176, "f16", "f16", "in place"),
+                                                (33000, 1300, 2176, "bf16", "f16", None)])
+def test_wgrad_16_bit_results_of_long_sequences(T, M, K, name, out, add):
+    """More tokens than one accumulator sums, in every form."""
+    check_wgrad(np.random.default_rng(20), T, M, K, name, out, add)
+
+
 def test_dgrad_agrees_with_differences_of_the_forward():
     """<C, gemm(x + e) - gemm(x - e)> / 2 against <dX, e>: the forward is linear
     in x (planes fixed), so the difference is the derivative but for both
