@@ -445,7 +445,7 @@ RB_API rb_status rb_unpack8(const uint8_t* codes, const float* scales, int64_t r
  *              none makes every output that it enters NaN, and rb_gemm_check
  *              reports it. 0: any fp32 scales; each block's product is
  *              scaled and summed in fp32 registers, which takes up to twice
- *              as long. fp32 outputs are computed in that way whatever
+ *              as long (xs ws itself may leave fp32's range). fp32 outputs are computed in that way whatever
  *              pow2_scales says.
  * w, w_scales  device, [M][K] codes and [ceil(M / 128)][K / 128] scales
  *              (rb_pack8 with block_rows = 128); codes 16-byte aligned.

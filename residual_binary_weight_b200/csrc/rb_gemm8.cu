@@ -42,6 +42,7 @@
 #include "rb_gemm8.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace rb {
 namespace {
@@ -93,6 +94,30 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+__device__ __forceinline__ bool normal(float f) {
+    return (__float_as_uint(f) & 0x7fffffffu) - 0x00800000u < 0x7f000000u;
+}
+
+// Whether a product of two scales may not be a normal fp32 value: from the
+// smallest and largest magnitudes (as bits) of either
+__device__ __forceinline__ bool products_leave_range(uint32_t x_lo, uint32_t x_hi, uint32_t w_lo, uint32_t w_hi) {
+    return min(x_lo, w_lo) < 0x00800000u || max(x_hi, w_hi) >= 0x7f800000u || (x_lo >> 23) + (w_lo >> 23) < 128u ||
+           (x_hi >> 23) + (w_hi >> 23) > 380u;
+}
+
+// A block's factor f = sx sw where it is not a normal value although both scales
+// are finite and not zero, in two steps, f after `first` (else first stays 1):
+// where it is too large, the smaller scale comes first (it is at least 1 then, so a
+// step that overflows has a result that does), where it is too small, the
+// larger one (below 2^23 then).
+__device__ __forceinline__ void two_factors(float sx, float sw, float& f, float& first) {
+    const float lo = fminf(fabsf(sx), fabsf(sw)), hi = fmaxf(fabsf(sx), fabsf(sw));
+    if (normal(f) || !(lo > 0.0f) || !(hi < INFINITY) || sx != sx || sw != sw) return;
+    const bool x_first = (fabsf(sx) == lo) == (fabsf(f) > 1.0f);
+    first = x_first ? sx : sw;
+    f = x_first ? sw : sx;
+}
+
 template <int FORM>
 __global__ void __launch_bounds__(G8Cfg<FORM>::THREADS, FORM == PAIR ? 1 : 2)
 gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
@@ -102,6 +127,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
     extern __shared__ __align__(1024) unsigned char dsm[];
     __shared__ __align__(8) uint64_t bars[2 * MAX_STAGES + 4 + 2 * SLOTS];
     __shared__ float staged[SLOTS][SLOT_FLOATS];
+    __shared__ uint32_t staged_apart[SLOTS];
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t abort_word;
     volatile uint32_t* abort_flag = &abort_word;
@@ -206,11 +232,11 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                     xr[k][4] = hi.x, xr[k][5] = hi.y, xr[k][6] = hi.z, xr[k][7] = hi.w;
                 } else {
 #pragma unroll
-                    for (int i = 0; i < SG; ++i) xr[k][i] = t < a.T && i < n ? __ldg(p + i) : 0.0f;
+                    for (int i = 0; i < SG; ++i) xr[k][i] = t < a.T && i < n ? __ldg(p + i) : 1.0f;
                 }
             }
             const int wb = min((row0(us) >> 7) + (lane & 3), w_blocks - 1);
-            wr = (lane >> 2) < n ? __ldg(a.ws + static_cast<int64_t>(wb) * a.G + gs + (lane >> 2)) : 0.0f;
+            wr = (lane >> 2) < n ? __ldg(a.ws + static_cast<int64_t>(wb) * a.G + gs + (lane >> 2)) : 1.0f;
         };
         int done = 0, slot = 0;
         uint32_t sph = 1u;
@@ -227,6 +253,18 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
 #pragma unroll
                     for (int k = 0; k < 4; ++k) staged[slot][i * TM + 32 * k + lane] = xr[k][i];
                 staged[slot][SG * TM + lane] = wr;
+                uint32_t x_lo = 0xffffffffu, x_hi = 0u;
+#pragma unroll
+                for (int i = 0; i < SG; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t e = __float_as_uint(xr[k][i]) & 0x7fffffffu;
+                        x_lo = min(x_lo, e), x_hi = max(x_hi, e);
+                    }
+                const uint32_t w_e = __float_as_uint(wr) & 0x7fffffffu;
+                const bool apart = products_leave_range(__reduce_min_sync(FULL_MASK, x_lo), __reduce_max_sync(FULL_MASK, x_hi),
+                                                        __reduce_min_sync(FULL_MASK, w_e), __reduce_max_sync(FULL_MASK, w_e));
+                if (lane == 0) staged_apart[slot] = apart;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sc_full(slot));
                 if (++slot == SLOTS) {
@@ -345,37 +383,51 @@ gemm8_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ C
                 const float* sw = staged[slot] + SG * TM;
                 const int n = min(SG, g_hi - gs);
                 float fx = sx[0], fw0 = sw[w0], fw1 = FORM == PAIR ? sw[w1] : fw0;
-                for (int gi = 0; gi < n; ++gi) {
-                    if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), bph, abort_flag, err, 8u))) {
-                        ok = false;
-                        break;
-                    }
-                    const float f0 = fx * fw0, f1 = FORM == PAIR ? fx * fw1 : f0;
-                    if (gi + 1 < n) {       // the next block's, on their way meanwhile
-                        fx = sx[(gi + 1) * TM];
-                        fw0 = sw[(gi + 1) * 4 + w0];
-                        fw1 = FORM == PAIR ? sw[(gi + 1) * 4 + w1] : fw0;
-                    }
-                    if (live) {
-                        fence_after();
-                        const uint32_t from = taddr + static_cast<uint32_t>(b * C::BUF);
-#pragma unroll
-                        for (int c = 0; c < 64 / CW; ++c) {
-                            if (c * CW < cols) {
-                                uint32_t v[CW];
-                                tmem_load<CW>(from + static_cast<uint32_t>(c * CW), v);
-                                if ((c + 1) * CW == cols) give_back(b);
-#pragma unroll
-                                for (int i = 0; i < CW; ++i)
-                                    acc[c * CW + i] = fmaf(__uint_as_float(v[i]), c * CW < 32 ? f0 : f1, acc[c * CW + i]);
-                            }
+                // apart: some factor sx sw of these blocks may not be a normal value
+                // (the scale warp has looked at all of the tile's; a look at each block's
+                // here would cost 4 to 8 %)
+                auto blocks = [&](auto apart) {
+                    for (int gi = 0; gi < n; ++gi) {
+                        if (!__all_sync(FULL_MASK, mbar_wait(acc_full(b), bph, abort_flag, err, 8u))) {
+                            ok = false;
+                            break;
                         }
-                    } else {
-                        give_back(b);
+                        float f0 = fx * fw0, f1 = FORM == PAIR ? fx * fw1 : f0, first0 = 1.0f, first1 = 1.0f;
+                        if constexpr (apart) {
+                            two_factors(fx, fw0, f0, first0);
+                            if (FORM == PAIR) two_factors(fx, fw1, f1, first1);
+                            else f1 = f0, first1 = first0;
+                        }
+                        if (gi + 1 < n) {       // the next block's, on their way meanwhile
+                            fx = sx[(gi + 1) * TM];
+                            fw0 = sw[(gi + 1) * 4 + w0];
+                            fw1 = FORM == PAIR ? sw[(gi + 1) * 4 + w1] : fw0;
+                        }
+                        if (live) {
+                            fence_after();
+                            const uint32_t from = taddr + static_cast<uint32_t>(b * C::BUF);
+#pragma unroll
+                            for (int c = 0; c < 64 / CW; ++c) {
+                                if (c * CW < cols) {
+                                    uint32_t v[CW];
+                                    tmem_load<CW>(from + static_cast<uint32_t>(c * CW), v);
+                                    if ((c + 1) * CW == cols) give_back(b);
+#pragma unroll
+                                    for (int i = 0; i < CW; ++i) {
+                                        const float p = __uint_as_float(v[i]) * (!apart ? 1.0f : c * CW < 32 ? first0 : first1);
+                                        acc[c * CW + i] = fmaf(p, c * CW < 32 ? f0 : f1, acc[c * CW + i]);
+                                    }
+                                }
+                            }
+                        } else {
+                            give_back(b);
+                        }
+                        b ^= 1;
+                        if (b == 0) bph ^= 1u;
                     }
-                    b ^= 1;
-                    if (b == 0) bph ^= 1u;
-                }
+                };
+                if (staged_apart[slot]) blocks(std::true_type{});
+                else blocks(std::false_type{});
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sc_empty(slot));

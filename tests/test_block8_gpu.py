@@ -222,6 +222,50 @@ def test_gemm8_scales_of_the_whole_range(T):
 
 
 @pytest.mark.parametrize("T", [5, 2100])
+@pytest.mark.parametrize("name,pow2", [("f32", True), ("f32", False), ("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("side", ["large", "small"])
+def test_gemm8_scales_whose_product_leaves_the_range(T, name, pow2, side):
+    """sx sw above 2^128 or below 2^-126 where the results are in range: of the
+    smallest codes (and rows of zeros), or of all. The factors' one rounding
+    more is within the bound's terms."""
+    rng = np.random.default_rng(35)
+    M, K = 2400, 256
+    w, ws = codes_of(rng, M, K, 128)
+    x, xs = codes_of(rng, T, K, 1)
+    if side == "large":
+        w, x = w & 0x81, x & 0x81                   # 0 and +-2^-9: sums of at most 2^-10
+        w[::7], x[::3] = 0, 0
+    ws = np.full_like(ws, 2.0 ** 70 if side == "large" else 2.0 ** -69)
+    xs = np.full_like(xs, 2.0 ** 62 if side == "large" else 2.0 ** -68)
+    if not pow2:
+        ws, xs = (np.float32(v * rng.uniform(1, 2, v.shape)).astype(np.float64) for v in (ws, xs))
+    flip = rng.integers(0, 2, (1, K // 128))        # either scale is the larger one
+    a, b = np.where(flip, 2.0 ** 20, 1.0), np.where(flip, 2.0 ** -20, 1.0)
+    ws, xs = ws * a, xs * b
+    y = rb.gemm8(*dev_codes(w, ws), *dev_codes(x, xs), y_dtype=NAMES[name], pow2_scales=pow2, check_device=True)
+    ref, D = block8.gemm8(w, ws, x, xs)
+    close(y, ref, gemm8_mx_tol(w, ws, x, xs) if pow2 and name != "f32" else gemm8_tol(D, K // 128), NAMES[name])
+
+
+@pytest.mark.parametrize("T", [5, 2100])
+@pytest.mark.parametrize("value", [0.0, 1e-40, 2.0 ** 127, float("inf")])
+def test_gemm8_a_far_scale_leaves_other_tokens_alone(T, value):
+    rng = np.random.default_rng(36)
+    wd, wsd = dev_codes(*codes_of(rng, 2400, 1280, 128, True))
+    x, xs = codes_of(rng, T, 1280, 1, True)
+    xd, xsd = dev_codes(x, xs)
+    good = rb.gemm8(wd, wsd, xd, xsd, pow2_scales=False, y_dtype=torch.float32)
+    xsd[3, 4] = value
+    y = rb.gemm8(wd, wsd, xd, xsd, pow2_scales=False, y_dtype=torch.float32, check_device=True)
+    if value < 1:                                  # then block 4 adds nothing that fp32 sees
+        xs[3, 4] = 0
+        ref, D = block8.gemm8(wd.view(torch.uint8).cpu().numpy(), f64(wsd), x[3:4], xs[3:4])
+        close(y[3:4], ref, gemm8_tol(D, 10), torch.float32)
+    y[3] = good[3]
+    assert torch.equal(y, good)
+
+
+@pytest.mark.parametrize("T", [5, 2100])
 @pytest.mark.parametrize("value", [3.0, -1.0, 0.0, float("inf"), float("nan"), 1e-40])
 def test_gemm8_scales_that_are_no_powers_of_two_are_told(T, value):
     rng = np.random.default_rng(32)
