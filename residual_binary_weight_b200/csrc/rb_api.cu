@@ -93,7 +93,7 @@ static rb_status check_blocks8(int64_t rows, int64_t K, const char* what) {
 // the header of the calls that can do without one
 static rb_status check_header(const void* workspace, size_t ws_bytes) {
     if (!workspace) return RB_OK;
-    if ( ws_bytes < GEMM_HEADER_BYTES || !aligned16(workspace))
+    if (ws_bytes < GEMM_HEADER_BYTES || !aligned16(workspace))
         return fail(RB_ERR_WORKSPACE, "workspace needs %zu bytes (16-byte aligned), got %zu", (size_t)GEMM_HEADER_BYTES,
                     ws_bytes);
     return RB_OK;
@@ -635,12 +635,13 @@ rb_status rb_gemm_check(const void* workspace, void* stream) {
     uint32_t flag = 0;
     rb_status st = read_flags(workspace, stream, "rb_gemm_check", &flag);
     if (st != RB_OK) return st;
-    if (flag == 16u)
-        return fail(RB_ERR_DEVICE, "rb_gemm8 kernel flag 0x10: a scale is not a power of two (its products are NaN)");
-    if (flag)
-        return fail(RB_ERR_DEVICE, "rb_gemm kernel flag 0x%x: a pipeline wait ran out in (%s%s%s%s)", flag,
+    if (flag & 15u)
+        return fail(RB_ERR_DEVICE, "rb_gemm kernel flag 0x%x: a pipeline wait ran out in (%s%s%s%s)%s", flag,
                     (flag & 1u) ? "X-tile producer " : "", (flag & 2u) ? "MMA issuer " : "",
-                    (flag & 4u) ? "operand expansion " : "", (flag & 8u) ? "epilogue" : "");
+                    (flag & 4u) ? "operand expansion " : "", (flag & 8u) ? "epilogue" : "",
+                    (flag & 16u) ? "; also, a scale of rb_gemm8 is not a power of two" : "");
+    if (flag)
+        return fail(RB_ERR_DEVICE, "rb_gemm8 kernel flag 0x%x: a scale is not a power of two (its products are NaN)", flag);
     return RB_OK;
 }
 

@@ -802,6 +802,15 @@ def test_check_reports_a_flag_and_the_next_call_clears_it():
         call()
 
 
+def test_check_reports_every_flag():
+    lib, ws = rb.load(), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for flag, parts in [(16, [b"power of two"]), (2, [b"MMA issuer"]), (18, [b"MMA issuer", b"power of two"]), (25, [b"X-tile", b"epilogue", b"power of two"])]:
+        ws.view(torch.int32)[1] = flag
+        assert lib.rb_gemm_check(ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == 6
+        message = lib.rb_last_error()
+        assert all(p in message for p in parts) and (b"ran out" in message) == (flag != 16), message
+
+
 def test_places_past_32_bits():
     """Rows whose byte (pack8, unpack8, wgrad) or element offsets pass 2^32."""
     g = torch.Generator(device="cuda").manual_seed(5)
