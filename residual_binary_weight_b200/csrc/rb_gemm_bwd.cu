@@ -39,15 +39,18 @@
 //
 // Measured (2048 tokens x 14336 x 4096, bf16; 1628 TFLOP/s is the measured bf16
 // peak in bursts, 1361 under the power cap, which both kernels reach, at 1.45 GHz):
-// dgrad, two paths, 197 us, 1220 TFLOP/s; wgrad without `add` 229 us, 1050
-// TFLOP/s; with an fp32 `add`, whose bytes take 36 us of HBM's time, 270 us.
-// dgrad of 16 tokens through 8192 x 8192: 24.5 us (stage cycle, see STAGE_CYCLES);
-// wgrad of 777 tokens x 256 x 256: 8.2 us (launch, fill and the ranks' sum).
+// dgrad, two paths, 198 us, 1214 TFLOP/s (to fp32 dX 214 us; four paths with fp16
+// scales per 128 columns 323 us: the expansion's work); wgrad to fp32 without
+// `add` 231 us, 1040 TFLOP/s, to bf16 223 us; with an fp32 `add`, whose bytes
+// take 36 us of HBM's time, 273 us.
+// dgrad of 16 tokens through 8192 x 8192: 24.4 us (stage cycle, see STAGE_CYCLES);
+// wgrad of 777 tokens x 256 x 256: 8.5 us (launch, fill and the ranks' sum).
 //
 // Rounding: dgrad's operand W^[i][j] is the exact sum of the scales (to fp32)
 // rounded once to dY's 16-bit type; wgrad's operand s c is exact in that type
 // for scales that are powers of two in its range, as rb_pack8 writes them,
-// and rounded to it otherwise. Products are exact, sums fp32.
+// and rounded to it otherwise. Products are exact, sums fp32, in segments (see
+// SEGMENT_F16).
 #include "rb_tc.cuh"
 
 #include <cuda_bf16.h>
@@ -121,6 +124,11 @@ struct BwCfg {
     static constexpr uint32_t TMEM_COLS = 2 * BN, SUM_COL = FORM == PAIR ? BN : 2 * BN, SUM_TMEM_COLS = FORM == PAIR ? 2 * BN : 4 * BN;
     static_assert(SUM_TMEM_COLS <= 512, "tensor memory");
     static_assert(SMEM + 512 <= 227 * 1024, "shared memory");
+    // The CTAs of a cluster wait for one another while they hold tensor memory.
+    // Beside one of these no CTA of another such kernel (rb_gemm8's take 97 KB
+    // or more) finds room on an SM: if together they wanted more than 512 columns,
+    // two clusters on two streams could each hold what the other waits for.
+    static_assert(FORM == ONE || SMEM >= 132u * 1024u, "another cluster's CTA may share the SM's tensor memory");
     static_assert(FORM != SPLIT || BN * 512u <= TILES, "a split tile's sums do not fit the rings");
 };
 

@@ -789,6 +789,35 @@ def test_first_calls_of_several_threads():
     assert out.returncode == 0 and out.stdout.strip() == "ok", (out.returncode, out.stdout, out.stderr)
 
 
+def test_products_of_every_form_on_four_streams():
+    """Clusters, pairs and single tiles that share SMs and their tensor memory
+    with the forward's kernels: every result as when it runs alone."""
+    rng = np.random.default_rng(41)
+    jobs = []
+    for T, M, K in [(3, 600, 1024), (1300, 2600, 2048), (70, 20000, 128), (100, 300, 9856)]:
+        w, ws = dev_codes(*codes_of(rng, M, K, 128))
+        x, xs = dev_codes(*codes_of(rng, T, K, 1))
+        planes, a = plane_case(rng, M, K, 2, 0, False)
+        p, al = torch.from_numpy(rows_to_sliced(planes).view(np.int32)).cuda(), torch.from_numpy(a).cuda()
+        X, dY = values(rng, T, K, "f16"), gradient(rng, T, M, torch.float16)
+        jobs.append([lambda w=w, ws=ws, x=x, xs=xs: rb.gemm8(w, ws, x, xs, y_dtype=torch.bfloat16),
+                     lambda w=w, ws=ws, x=x, xs=xs: rb.gemm8(w, ws, x, xs, y_dtype=torch.float32),
+                     lambda d=dY, x=x, xs=xs: rb.gemm_wgrad(d, x, xs), lambda p=p, al=al, d=dY, K=K: rb.gemm_dgrad(p, al, d, K),
+                     lambda p=p, al=al, d=dY, K=K: rb.gemm_dgrad(p, al, d, K, dx_dtype=torch.float32),
+                     lambda p=p, al=al, X=X: rb.gemm(p, al, X, y_dtype=torch.float32)])
+    want = [[f().view(torch.uint8) for f in j] for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for i in range(24):
+        for k, (s, j) in enumerate(zip(streams, jobs)):
+            with torch.cuda.stream(s):
+                got[k].append(((i + k) % len(j), j[(i + k) % len(j)]()))
+    torch.cuda.synchronize()
+    for k, g in enumerate(got):
+        assert all(torch.equal(y.view(torch.uint8), want[k][n]) for n, y in g), k
+
+
 def test_check_reports_a_flag_and_the_next_call_clears_it():
     W, ws, X, dY, planes, alpha, bufs = case = _step_case(27)
     _step(*case)
