@@ -405,7 +405,8 @@ RB_API rb_status rb_gemv_check(const void* workspace, void* stream);
  * for each block of block_rows x 128 of them, [ceil(rows / block_rows)][K / 128];
  * a value is code * scale. block_rows is 1 (activations) or 128 (weights; the
  * last block may have fewer rows). K is a positive multiple of 128, and
- * rows * (K / 128) < 2^31.
+ * rows * (K / 128) < 2^31. No output may share bytes with an input (but
+ * rb_gemm_wgrad's `add`).
  */
 
 /*
@@ -439,6 +440,8 @@ RB_API rb_status rb_unpack8(const uint8_t* codes, const float* scales, int64_t r
  * cores, any number of tokens:
  *     y[t][m] = sum_g xs[t][g] ws[m / 128][g] sum_{j in block g} x[t][j] w[m][j]
  * (g = 0 .. K / 128 - 1), every sum in fp32.
+ * (Where the tensor cores apply the scales they also sum over all of K, and cut
+ * low bits off towards zero: about 5e-10 of the terms' magnitudes a column.)
  *
  * pow2_scales  1: every scale is a power of two, as rb_pack8 writes them; the
  *              tensor cores then apply them (16-bit outputs). A scale that is

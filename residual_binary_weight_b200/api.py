@@ -570,6 +570,9 @@ def gemm_wgrad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, add:
     (exact for a checkpoint of a tensor of that type); sums are fp32, and dW is
     rounded once (fp32 dW: once for each 1024 or 2048 tokens, and sums below
     2^-126 may become zero).
+
+    dY's rows must start on 16-byte boundaries. Where M is not a multiple of 8,
+    that takes a buffer with longer rows, torch.empty(T, -(-M // 8) * 8)[:, :M].
     """
     lib = _lib._lib or _lib.load()
     dev = _cuda_device(dY, codes, scales, add, dW, workspace)
@@ -603,7 +606,11 @@ def gemm_dgrad(planes: torch.Tensor, alpha: torch.Tensor, dY: torch.Tensor, K: i
     """Gradient of gemm() with respect to its input: dX = dY W^ with
     W^ = sum_k alpha_k (.) B_k taken straight from the planes, dY fp16 or bf16
     [T, M]. K is the layer's input width (sliced planes are padded to 512
-    columns, so they do not say it)."""
+    columns, so they do not say it).
+
+    W^ is rounded once to dY's type (so dX is within eps / 2 of the sum of its
+    terms' magnitudes); sums are fp32. dY's rows must start on 16-byte boundaries, as
+    gemm_wgrad's."""
     lib = _lib._lib or _lib.load()
     dev = _cuda_device(planes, alpha, dY, dX, workspace)
     N, M, order = _planes_geometry(planes, K)

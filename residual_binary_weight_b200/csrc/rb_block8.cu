@@ -14,10 +14,10 @@
 //
 // Both kernels are bound by HBM: 2 (or 4) bytes in and 1 byte out for each
 // value, 1/32 byte of scales, and the reverse. Measured, with a copy's 6539
-// GB/s as the peak: pack8 of 11008 x 4096 fp32 in 128 x 128 blocks 35.0 us
-// (98 %), of 2048 x 14336 bf16 16.0 us (85 %; 13.6 us are one pass, the rest
-// the launch and the last wave); unpack8 of 8192 x 11008 to bf16 43.9 us
-// (95 %). One row of 4096: 2.2 us, nearly all of it the launch.
+// GB/s as the peak: pack8 of 11008 x 4096 fp32 in 128 x 128 blocks 35.2 us
+// (98 %), of 2048 x 14336 bf16 15.8 us (86 %; 13.6 us are one pass, the rest
+// the launch and the last wave); unpack8 of 8192 x 11008 to bf16 44.2 us
+// (95 %). One row of 4096: 2.0 us, nearly all of it the launch.
 #include "rb_internal.cuh"
 
 #include <cuda_bf16.h>

@@ -32,9 +32,11 @@
 // block, they cost a sector for every 4 bytes and each of the 4 column slices,
 // which took four times as long as the MMAs.
 //
-// Measured (fp32 outputs): 2048 tokens x 14336 x 4096 189 us, 1270 TFLOP/s; the
-// promotion's instructions bound it (1300 cycles of each block, whose MMAs take
-// 450).
+// Measured (fp32 outputs): 2048 tokens x 14336 x 4096 190 us, 1265 TFLOP/s: 1300
+// cycles of each block, whose MMAs take 450. The promotion bounds it, by latency:
+// its about 100 instructions a warp and block are 400 issue cycles of 16 warps on
+// four schedulers, the rest four loads from tensor memory, each waited for before
+// the next, and the buffer's way back to the CTA that issues the MMAs.
 //
 // Roles: the epilogue warps (16 in a pair's CTA, else 8; warp w reads the
 // lanes of quarter w % 4 and the columns from 64 (w / 4) on), one TMA and

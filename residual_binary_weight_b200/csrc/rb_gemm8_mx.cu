@@ -7,10 +7,10 @@
 // and of B by an 8-bit exponent of that row, kept in tensor memory, so sums
 // run through all of K in the fp32 accumulator and the epilogue only sees the
 // finished tile. (The kernel of rb_gemm8.cu adds every 128 columns' product to
-// sums in registers: about 100 instructions of each epilogue warp for each
-// block, 1300 cycles where the MMAs take 450.) The accumulator's sums are
-// exact to about 1e-6 of the result, as those of rb_gemm, so fp32 outputs stay
-// with that kernel.
+// sums in registers, 1300 cycles of each block where the MMAs take 450.) The
+// accumulator cuts low bits off towards zero at every MMA, about 5e-10 of the
+// terms' magnitudes a column (7e-5 after 131072 columns of one sign), so fp32
+// outputs stay with that kernel; 16-bit outputs round far more away at any K in use.
 //
 // An exponent byte e stands for 2^(e - 127): the exponent field of the fp32
 // scale. Row r's byte lies in tensor-memory lane r % 32 (of each quarter),
@@ -20,11 +20,11 @@
 // tiles arrive by TMA. A scale that is no power of two gets the byte 255
 // (NaN): every output that it enters is NaN, and the error word says why.
 //
-// Measured: 2048 tokens x 14336 x 4096 to bf16 111 us, 2170 TFLOP/s (94 us in
+// Measured: 2048 tokens x 14336 x 4096 to bf16 112 us, 2150 TFLOP/s (96 us in
 // short bursts; under load the power cap holds the SMs near 1.3 GHz; the kernel
-// with sums in registers takes 189 us); 16 tokens x 28672 x 8192 44.7 us, 5.3 TB/s of
-// the weight's bytes (81 % of a copy's rate: the first and last loads of one wave
-// of tiles are not overlapped); one token x 4096 x 4096 8.1 us, of which HBM takes
+// with sums in registers takes 190 us); 16 tokens x 28672 x 8192 45.1 us, 5.2 TB/s of
+// the weight's bytes (80 % of a copy's rate: the first and last loads of one wave
+// of tiles are not overlapped); one token x 4096 x 4096 8.3 us, of which HBM takes
 // 2.6 (launch, fill of the rings, sum over the cluster).
 //
 // Forms as in rb_gemm8.cu: PAIR (two accumulators of up to 224 columns, TMA
